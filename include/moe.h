@@ -351,6 +351,55 @@ size_t moe_stack_workspace_size(const moe_layer* layers, const moe_prerouter* he
                                 int32_t K, int32_t K_next);
 
 /*
+ * 8-bit integer products.  The matrices around the routed layer (projections of
+ * the residual stream, an output head) as signed 8-bit codes with one fp32
+ * scale per output channel, against activations in signed 8-bit codes with one
+ * fp32 scale per token:
+ *   out[t][n] = qscale[t] * scale[n] * sum_k q[t][k] * codes[n][k] + bias[n]
+ * The sum is exact (32-bit integers; in_dim <= MOE_I8_MAX_IN), the rest is
+ * fp32, rounded once more where out is bf16.
+ * Row format: row i at base + i*ld bytes, in_dim codes, ld a multiple of 16
+ *   and at least moe_i8_row_bytes(in_dim), bases 16-byte aligned.  The bytes
+ *   of a codes row from in_dim to moe_i8_row_bytes(in_dim) must be zero; those
+ *   of a q row may hold anything (they are read and have no effect).
+ */
+#define MOE_I8_MAX_IN 65536
+#define MOE_I8_MAX_OUT 1048576
+
+typedef struct {
+  const int8_t* codes;  /* [out_dim] rows */
+  int64_t ld;           /* bytes from one row to the next */
+  const float* scale;   /* [out_dim] */
+  const float* bias;    /* [out_dim], or NULL */
+  int32_t out_dim, in_dim;
+} moe_linear8;
+
+/* Bytes a row of n codes takes (n rounded up to a multiple of 16); 0 for n < 1 or n > MOE_I8_MAX_IN (host). */
+size_t moe_i8_row_bytes(int32_t n);
+
+/*
+ * Activations to 8-bit codes, one scale per token:
+ *   m_t = max_k |x[t][k]|;  q[t][k] = 127 x[t][k] / m_t rounded to the nearest
+ *   integer, ties to even (of the exact quotient);  scale[t] = m_t / 127.
+ * eps >= 0 quantises rmsnorm(x) instead (as moe_rmsnorm_bf16 without its
+ * rounding to bf16): the codes stay the same and
+ *   scale[t] = m_t / sqrt(mean_k x[t][k]^2 + eps) / 127;  eps < 0: no norm.
+ * x [T][H] fp32 (x_type 0) or bf16 (x_type 1); q [T] rows of ldq bytes (bytes
+ * past H are not written); scale [T] fp32.  A row of zeros gets codes 0 and
+ * scale 0; a row holding an infinity or a NaN gets codes 0 and scale NaN, so
+ * that what is computed from it is NaN.  H <= MOE_I8_MAX_IN.
+ */
+moe_status moe_quant_i8(const void* x, int32_t x_type, int32_t T, int32_t H, float eps, int8_t* q, int64_t ldq,
+                        float* scale, void* stream);
+
+/*
+ * The product above for T tokens: q [T] rows of ldq bytes, qscale [T], out
+ * [T][out_dim].  out_mode 0: fp32; 1: bf16; 2: fp32, added to what out holds.
+ */
+moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, const float* qscale, int32_t T, void* out,
+                         int32_t out_mode, int32_t* err_word, void* stream);
+
+/*
  * Allocation-free variant of moe_expert_forward.  The pages have no
  * counterpart: this exists for callers that cannot allocate device memory for
  * a workspace -- e.g. a host framework that owns every device allocation and

@@ -13,7 +13,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from .weights import DeviceHead, DeviceLayer, DeviceStack, block_bytes, block_stride, host_pool, qrow_bytes  # noqa: F401
+from .weights import DeviceHead, DeviceLayer, DeviceLinear8, DeviceStack, block_bytes, block_stride, host_pool, qrow_bytes  # noqa: F401
 
 OUT_F32, OUT_BF16, OUT_ADD_F32 = 0, 1, 2
 
@@ -176,6 +176,56 @@ def prerouter_predict(head: DeviceHead, u: torch.Tensor, sel: torch.Tensor, K_ne
     err = _arg(fn, "err_word", err_word, I32, 1, optional=True)
     _check(fn, lib().prerouter_predict(ctypes.byref(P), _p(u), args[0], T, K, *args[1:], *_ws(fn, workspace), err,
                                        _stream(stream)))
+
+
+I8 = (torch.int8,)
+
+
+def moe_i8_row_bytes(n: int) -> int:
+    return lib().moe_i8_row_bytes(n)
+
+
+def _i8_rows(fn: str, name: str, q, width: int) -> tuple[int, int, int]:
+    """(address, row bytes, rows) of an 8-bit code tensor ``[T, ld]`` whose rows hold ``width`` codes."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError(f"{fn}: {name} must be [T, ld]")
+    p = _arg(fn, name, q, I8)
+    if q.shape[1] % 16 or q.shape[1] < width:
+        raise ValueError(f"{fn}: {name} rows hold {q.shape[1]} bytes, need a multiple of 16 that holds {width}")
+    return p, q.shape[1], q.shape[0]
+
+
+def moe_quant_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, eps: float | None = None, stream=None):
+    """8-bit codes and one scale per token of ``x`` ``[T, H]`` (fp32 or bf16), or with ``eps`` of rmsnorm(x).
+
+    ``q`` int8 ``[T, ld]`` with ``ld`` a multiple of 16 (``moe_i8_row_bytes(H)`` or more), ``scale`` fp32 ``[T]``.
+    """
+    fn = "moe_quant_i8"
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{fn}: x must be [T, H]")
+    if eps is not None and not eps >= 0:
+        raise ValueError(f"{fn}: eps must be >= 0, got {eps}")
+    T, H = x.shape
+    px = _arg(fn, "x", x, F32 + (torch.bfloat16,))
+    pq, ld, rows = _i8_rows(fn, "q", q, H)
+    if rows < T:
+        raise ValueError(f"{fn}: q has {rows} rows, x has {T}")
+    ps = _arg(fn, "scale", scale, F32, T)
+    _check(fn, lib().moe_quant_i8(px, int(x.dtype == torch.bfloat16), T, H, -1.0 if eps is None else eps, pq, ld, ps,
+                                  _stream(stream)))
+
+
+def moe_linear_i8(linear: DeviceLinear8, q: torch.Tensor, qscale: torch.Tensor, out: torch.Tensor, out_mode: int,
+                  err_word: torch.Tensor | None = None, stream=None):
+    """``out [T, out_dim] = qscale[t] scale[n] sum_k q[t,k] codes[n,k] + bias[n]`` for the ``T`` rows of ``q``."""
+    fn, W = "moe_linear_i8", linear.struct
+    pq, ld, T = _i8_rows(fn, "q", q, W.in_dim)
+    ps = _arg(fn, "qscale", qscale, F32, T)
+    po = _arg(fn, "out", out, BF16_BITS if out_mode == OUT_BF16 else F32, T * W.out_dim)
+    if linear.device != q.device:
+        raise ValueError(f"{fn}: the matrix is on {linear.device}, q on {q.device}")
+    err = _arg(fn, "err_word", err_word, I32, 1, optional=True)
+    _check(fn, lib().moe_linear_i8(ctypes.byref(W), pq, ld, ps, T, po, out_mode, err, _stream(stream)))
 
 
 class TieredPool:

@@ -35,6 +35,11 @@ class moe_prerouter(ctypes.Structure):
                 ("H", c_int32), ("E", c_int32), ("P", c_int32), ("E_next", c_int32)]
 
 
+class moe_linear8(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("ld", c_int64), ("scale", c_void_p), ("bias", c_void_p), ("out_dim", c_int32),
+                ("in_dim", c_int32)]
+
+
 class moe_tier_stats(ctypes.Structure):
     _fields_ = [(n, c_int64) for n in ("acquires", "requested", "hits", "prefetch_hits", "misses", "prefetched",
                                        "bytes_acquired", "bytes_prefetched")]
@@ -67,6 +72,10 @@ SIGNATURES = {
     "moe_tier_release": (c_int32, [c_void_p, c_void_p]),
     "moe_tier_prefetch": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p]),
     "moe_tier_get_stats": (c_int32, [c_void_p, POINTER(moe_tier_stats)]),
+    "moe_i8_row_bytes": (c_size_t, [c_int32]),
+    "moe_quant_i8": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
+    "moe_linear_i8": (c_int32, [POINTER(moe_linear8), c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_int32,
+                                c_void_p, c_void_p]),
     "moe_stack_grid": (c_int32, []),
     "moe_stack_workspace_size": (c_size_t, [POINTER(moe_layer), POINTER(moe_prerouter), c_int32, c_int32, c_int32,
                                             c_int32]),

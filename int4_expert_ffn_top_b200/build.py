@@ -8,7 +8,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmoe.so")
-SOURCES = [os.path.join(HERE, "csrc", "moe_api.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("moe_api.cu", "linear_api.cu")]
 DEPS = SOURCES + [os.path.join(HERE, "csrc", f) for f in os.listdir(os.path.join(HERE, "csrc"))] + [
     os.path.join(ROOT, "include", "moe.h")]
 

@@ -159,6 +159,33 @@ class DeviceLayer:
         return L
 
 
+class DeviceLinear8:
+    """An 8-bit matrix on the device and its ``moe_linear8`` struct.
+
+    ``codes`` int8 ``[out, in]``, ``scale`` (one per output channel) and ``bias`` (optional) fp32 ``[out]``, all on
+    one CUDA device.  Rows are laid out once, zero-padded to a multiple of 16 bytes; a matrix that has that form
+    already (contiguous, ``in`` a multiple of 16) is used as it is.
+    """
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor | None = None):
+        if codes.dim() != 2 or codes.dtype != torch.int8 or codes.numel() == 0:
+            raise ValueError("DeviceLinear8: codes must be a non-empty int8 [out, in] tensor")
+        n, k = codes.shape
+        for name, t in (("scale", scale), ("bias", bias)):
+            if t is not None and (t.dtype != torch.float32 or t.shape != (n,) or t.device != codes.device):
+                raise ValueError(f"DeviceLinear8: {name} must be float32 [{n}] on {codes.device}")
+        ld = (k + 15) // 16 * 16
+        if ld != k or not codes.is_contiguous() or codes.data_ptr() % 16:
+            rows = torch.zeros((n, ld), dtype=torch.int8, device=codes.device)
+            rows[:, :k] = codes
+            codes = rows
+        self.codes, self.scale = codes, scale.contiguous()
+        self.bias = None if bias is None else bias.contiguous()
+        self.out_dim, self.in_dim = n, k
+        self.device = codes.device
+        self.struct = _lib.moe_linear8(codes.data_ptr(), ld, self.scale.data_ptr(), _ptr(self.bias), n, k)
+
+
 class DeviceHead:
     """One Prerouter head on the device and its ``moe_prerouter`` struct."""
 

@@ -1,0 +1,194 @@
+"""GPU parity of the 8-bit product and its quantiser against integer and 64-bit definitions.
+
+Codes are compared exactly with the correctly rounded quotient (rational arithmetic where 64 bits tie), integer sums
+are exact, so the only allowance is for the fp32 steps around them: EPS32 each.
+"""
+import numpy as np
+import pytest
+import torch
+
+import int4_expert_ffn_top_b200 as M
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+EPS32 = torch.finfo(torch.float32).eps / 2
+EPSBF = torch.finfo(torch.bfloat16).eps / 2
+
+
+def codes_of(x):
+    """round_half_even(127 x / max|x|) per row, in 64 bits: 127 x is exact there, and a quotient of two fp32 values
+    that is not a tie is further from one than a double's rounding."""
+    x = x.double()
+    m = x.abs().amax(1, keepdim=True)
+    return torch.where(m > 0, (127 * x / torch.where(m > 0, m, torch.ones_like(m))).round(), torch.zeros_like(x)), m[:, 0]
+
+
+def quant(x, eps=None, pad=0, fill=77):
+    T, H = x.shape
+    ld = M.moe_i8_row_bytes(H) + 16 * pad
+    q = torch.full((T, ld), fill, dtype=torch.int8, device=DEV)
+    s = torch.full((T,), float("nan"), device=DEV)
+    M.moe_quant_i8(x, q, s, eps=eps)
+    torch.cuda.synchronize()
+    assert (q[:, H:] == fill).all()  # bytes past the row stay
+    return q, s
+
+
+def linear(N, K, seed=0, bias=True):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    W = torch.randint(-128, 128, (N, K), dtype=torch.int8, device=DEV, generator=g)
+    sw = torch.rand(N, device=DEV, generator=g) * 0.01 + 1e-4
+    b = torch.randn(N, device=DEV, generator=g) if bias else None
+    return M.DeviceLinear8(W, sw, b), W, sw, b
+
+
+def product64(W, sw, b, q, sx, K):
+    p = (q[:, :K].double() @ W.double().T) * sx.double()[:, None] * sw.double()
+    return p, p if b is None else p + b.double()
+
+
+def check_linear(N, K, T, mode, bias=True, pad=0, seed=0):
+    lin, W, sw, b = linear(N, K, seed, bias)
+    g = torch.Generator(device=DEV).manual_seed(seed + 1)
+    q = torch.randint(-128, 128, (T, M.moe_i8_row_bytes(K) + 16 * pad), dtype=torch.int8, device=DEV, generator=g)
+    sx = torch.rand(T, device=DEV, generator=g) * 0.1
+    tail = 64
+    out = torch.full((T * N + tail,), 3.0, device=DEV, dtype=torch.bfloat16 if mode == M.OUT_BF16 else torch.float32)
+    if mode == M.OUT_ADD_F32:
+        out[:T * N] = torch.randn(T * N, device=DEV, generator=g)
+    before = out.clone()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    M.moe_linear_i8(lin, q, sx, out, mode, err_word=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    p, ref = product64(W, sw, b, q, sx, K)
+    # int -> fp32, two scales, the bias: one rounding each
+    tol = 3.01 * EPS32 * p.abs() + 1.01 * EPS32 * ref.abs()
+    if mode == M.OUT_BF16:
+        tol = tol + 1.01 * EPSBF * ref.abs()
+    elif mode == M.OUT_ADD_F32:
+        ref = ref + before[:T * N].view(T, N).double()
+        tol = tol + 1.01 * EPS32 * ref.abs()
+    off = (out[:T * N].view(T, N).double() - ref).abs() - tol
+    assert off.max().item() <= 0, off.max().item()
+    assert torch.equal(out[T * N:], before[T * N:])  # nothing written behind the last row
+
+
+# ----------------------------------------------------------------------------- quantiser
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 17), (5, 2048), (2, 1000), (7, 255), (1, 65536), (300, 4096), (2, 9999)])
+def test_codes_are_the_correctly_rounded_quotients(cuda_ok, T, H, dtype):
+    g = torch.Generator(device=DEV).manual_seed(T * H)
+    x = (torch.randn((T, H), device=DEV, generator=g) * torch.rand((T, 1), device=DEV, generator=g).add(0.1)).to(dtype)
+    for eps in (None, 1e-6):
+        q, s = quant(x, eps, pad=T % 2)
+        ref, m = codes_of(x)
+        assert torch.equal(q[:, :H].double(), ref)
+        if eps is not None:
+            m = m / (x.double().square().mean(1) + eps).sqrt()
+        # the sum of squares: H/256 terms a thread, 5 + 8 joining steps, each one rounding, halved by the root;
+        # then mean, eps, root, reciprocal, product and /127
+        tol = (0.5 * (H / 256 + 16) + 6 if eps is not None else 1) * 1.01 * EPS32
+        assert ((s.double() * 127 / m) - 1).abs().max().item() <= tol
+
+
+def test_codes_at_ties_and_next_to_them(cuda_ok):
+    """m = 254 puts x = n + 1/2 steps exactly between two codes at odd integers; its neighbours lie to either side."""
+    n = torch.arange(-253, 254, 2, dtype=torch.float32)
+    x = torch.cat([n, torch.nextafter(n, n + 1), torch.nextafter(n, n - 1), torch.tensor([254.0, -254.0])])[None]
+    q, _ = quant(x.to(DEV))
+    h = (x[0].numpy().astype(np.float64) / 2)
+    assert np.array_equal(q[0, :x.shape[1]].cpu().numpy(), np.rint(h).astype(np.int8))
+    assert np.array_equal(np.rint(h[:254]) % 2, np.zeros(254))  # the ties go to even codes
+
+
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 1e-30, 1e30, 3e38])
+def test_extreme_magnitudes(cuda_ok, scale):
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = (torch.rand((4, 100), device=DEV, generator=g) * 2 - 1) * scale
+    q, s = quant(x)
+    ref, m = codes_of(x)
+    assert torch.equal(q[:, :100].double(), ref)
+    assert ((s.double() - m / 127).abs() <= EPS32 * 1.01 * m / 127 + 2.0 ** -150).all()
+
+
+def test_zero_and_non_finite_rows(cuda_ok):
+    x = torch.randn((6, 70), device=DEV)
+    x[0] = 0
+    x[1, 3] = float("nan")
+    x[2, 69] = float("inf")
+    x[3, 0] = float("-inf")
+    x[4, 5], x[4, 6] = float("nan"), float("inf")
+    for eps in (None, 0.0):
+        q, s = quant(x, eps)
+        assert (q[:5, :70] == 0).all() and s[0].item() == 0 and torch.isnan(s[1:5]).all() and torch.isfinite(s[5])
+        assert torch.equal(q[5:, :70].double(), codes_of(x[5:])[0])
+
+
+# ----------------------------------------------------------------------------- product
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("N,K,T", [(1, 1, 1), (16, 64, 1), (17, 63, 3), (2051, 1000, 13), (4096, 2048, 1), (33, 65, 8),
+                                   (100, 4096, 9), (257, 129, 16), (48, 333, 31), (640, 2048, 64), (300, 144, 65),
+                                   (129, 255, 127), (256, 512, 128), (513, 1040, 300), (2048, 2048, 256)])
+def test_product(cuda_ok, N, K, T, mode):
+    check_linear(N, K, T, mode, bias=(N + T) % 2 == 0, pad=T % 3, seed=N + T)
+
+
+@pytest.mark.parametrize("T", [1, 70, 130])
+def test_largest_sum_is_exact(cuda_ok, T):
+    """All codes -128 over the longest rows: the largest magnitude a 32-bit sum has to hold."""
+    K, N = 65536, 20
+    lin = M.DeviceLinear8(torch.full((N, K), -128, dtype=torch.int8, device=DEV), torch.ones(N, device=DEV))
+    q = torch.full((T, K), -128, dtype=torch.int8, device=DEV)
+    out = torch.empty((T, N), device=DEV)
+    M.moe_linear_i8(lin, q, torch.ones(T, device=DEV), out, M.OUT_F32)
+    assert (out == float(128 * 128 * K)).all()
+
+
+def test_non_finite_scales_stay_in_their_rows(cuda_ok):
+    lin, W, sw, b = linear(40, 64)
+    for T in (3, 130):
+        q = torch.ones((T, 64), dtype=torch.int8, device=DEV)
+        sx = torch.ones(T, device=DEV)
+        sx[1] = float("nan")
+        out = torch.empty((T, 40), device=DEV)
+        M.moe_linear_i8(lin, q, sx, out, M.OUT_F32)
+        assert torch.isnan(out[1]).all() and torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()
+
+
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_quantised_projection_as_used(cuda_ok, T):
+    """Residual stream -> normed codes -> product added to the residual, against 64 bits, eagerly on another stream
+    and replayed from a graph."""
+    H, N = 512, 512
+    lin, W, sw, _ = linear(N, H, bias=False)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn((T, H), device=DEV, generator=g)
+    q = torch.zeros((T, H), dtype=torch.int8, device=DEV)
+    s = torch.empty(T, device=DEV)
+    out = x.clone()
+
+    def call():
+        M.moe_quant_i8(x, q, s, eps=1e-6)
+        M.moe_linear_i8(lin, q, s, out, M.OUT_ADD_F32)
+
+    ref, m = codes_of(x)
+    unit = m / (x.double().square().mean(1) + 1e-6).sqrt() / 127
+    p = (ref @ W.double().T) * unit[:, None] * sw.double()
+    # the scale's roundings (see above) and the product's
+    tol = ((0.5 * (H / 256 + 16) + 6) + 3) * 1.01 * EPS32 * p.abs() + 1.01 * EPS32 * (p + x.double()).abs()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    assert ((out.double() - x.double() - p).abs() <= tol).all()
+    first = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    out.copy_(x)
+    q.fill_(5)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)

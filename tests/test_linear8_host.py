@@ -1,0 +1,102 @@
+"""CPU checks of the 8-bit product: layout, argument order of the binding, refusals before any launch."""
+import ctypes
+
+import pytest
+import torch
+
+import int4_expert_ffn_top_b200 as M
+from int4_expert_ffn_top_b200 import _lib
+from int4_expert_ffn_top_b200 import build as B
+from test_binding_checks import cu, f32, i32, rec  # noqa: F401  (fixture)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return _lib.load()
+
+
+def test_row_bytes(lib):
+    assert [lib.moe_i8_row_bytes(n) for n in (0, -3, 1, 16, 17, 65536, 65537)] == [0, 0, 16, 16, 32, 65536, 0]
+
+
+def test_rows_are_padded_with_zeros_once():
+    codes = torch.randint(-128, 128, (5, 19), dtype=torch.int8)
+    d = M.DeviceLinear8(codes, torch.ones(5))
+    assert d.codes.shape == (5, 32) and torch.equal(d.codes[:, :19], codes) and (d.codes[:, 19:] == 0).all()
+    assert (d.struct.ld, d.struct.out_dim, d.struct.in_dim, d.struct.bias) == (32, 5, 19, None)
+    whole = torch.zeros((4, 32), dtype=torch.int8)
+    assert M.DeviceLinear8(whole, torch.ones(4)).codes.data_ptr() == whole.data_ptr()
+    turned = torch.randint(-128, 128, (32, 16), dtype=torch.int8).T
+    assert torch.equal(M.DeviceLinear8(turned, torch.ones(16)).codes, turned)
+    for bad in (lambda: M.DeviceLinear8(codes.float(), torch.ones(5)), lambda: M.DeviceLinear8(codes, torch.ones(4)),
+                lambda: M.DeviceLinear8(codes, torch.ones(5), torch.ones(5).double()),
+                lambda: M.DeviceLinear8(codes[:0], torch.ones(0))):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_library_refuses_bad_calls(lib):
+    bad, uns = _lib.MOE_ERR_INVALID_ARG, _lib.MOE_ERR_UNSUPPORTED
+    A = 1 << 20
+
+    def quant(x=A, kind=0, T=1, H=64, eps=-1.0, q=A, ld=64, scale=A):
+        return lib.moe_quant_i8(x, kind, T, H, eps, q, ld, scale, None)
+
+    assert quant(T=0) == _lib.MOE_OK and quant(T=0, x=None, q=None, scale=None) == _lib.MOE_OK
+    for kw in (dict(kind=2), dict(eps=float("nan")), dict(ld=48), dict(ld=72), dict(x=None), dict(q=None),
+               dict(q=A + 8), dict(scale=None)):
+        assert quant(**kw) == bad, kw
+    for kw in (dict(T=-1), dict(T=_lib.MOE_MAX_TOKENS + 1), dict(H=0), dict(H=65537, ld=65552)):
+        assert quant(**kw) == uns, kw
+
+    def product(codes=A, ld=64, scale=A, n=8, k=64, q=A, ldq=64, qs=A, T=1, out=A, mode=0):
+        W = _lib.moe_linear8(codes, ld, scale, None, n, k)
+        return lib.moe_linear_i8(ctypes.byref(W), q, ldq, qs, T, out, mode, None, None)
+
+    assert product(T=0) == _lib.MOE_OK and product(T=0, q=None, qs=None, out=None) == _lib.MOE_OK
+    assert lib.moe_linear_i8(None, A, 64, A, 1, A, 0, None, None) == bad
+    for kw in (dict(codes=None), dict(codes=A + 4), dict(ld=48), dict(ld=70), dict(scale=None), dict(q=None),
+               dict(q=A + 1), dict(ldq=32), dict(ldq=65), dict(qs=None), dict(out=None), dict(mode=3), dict(mode=-1)):
+        assert product(**kw) == bad, kw
+    for kw in (dict(T=-1), dict(T=_lib.MOE_MAX_TOKENS + 1), dict(n=0), dict(n=1048577), dict(k=0),
+               dict(k=65537, ld=65552, ldq=65552)):
+        assert product(**kw) == uns, kw
+
+
+class FakeLinear:
+    def __init__(self, n, k):
+        self.struct = _lib.moe_linear8(1 << 20, (k + 15) // 16 * 16, 1 << 20, None, n, k)
+        self.device = torch.device("cuda", 0)
+
+
+def i8(*shape):
+    return cu(torch.zeros(shape, dtype=torch.int8))
+
+
+def test_binding_order_and_checks(rec):  # noqa: F811
+    x, q, s = f32(5, 60), i8(5, 64), f32(5)
+    M.moe_quant_i8(x, q, s, stream=0)
+    assert rec.calls[-1] == ("moe_quant_i8", (x.data_ptr(), 0, 5, 60, -1.0, q.data_ptr(), 64, s.data_ptr(), 0))
+    xb = cu(torch.zeros((5, 60), dtype=torch.bfloat16))
+    M.moe_quant_i8(xb, q, s, eps=1e-5, stream=0)
+    assert rec.calls[-1][1][1:5] == (1, 5, 60, 1e-5)
+    lin, out = FakeLinear(7, 60), f32(5, 7)
+    M.moe_linear_i8(lin, q, s, out, M.OUT_ADD_F32, stream=0)
+    assert rec.calls[-1][1][1:] == (q.data_ptr(), 64, s.data_ptr(), 5, out.data_ptr(), 2, None, 0)
+    err = i32(1)
+    out16 = cu(torch.zeros((5, 7), dtype=torch.int16))
+    M.moe_linear_i8(lin, q, s, out16, M.OUT_BF16, err_word=err, stream=0)
+    assert rec.calls[-1][1][-4:] == (out16.data_ptr(), 1, err.data_ptr(), 0)
+    n = len(rec.calls)
+    for call in (lambda: M.moe_quant_i8(x, i8(5, 62), s), lambda: M.moe_quant_i8(x, i8(5, 48), s),
+                 lambda: M.moe_quant_i8(x, i8(4, 64), s), lambda: M.moe_quant_i8(x, q, f32(4)),
+                 lambda: M.moe_quant_i8(x.double(), q, s), lambda: M.moe_quant_i8(x, q, s, eps=-1.0),
+                 lambda: M.moe_quant_i8(x, q, s, eps=float("nan")), lambda: M.moe_quant_i8(x[0], q, s),
+                 lambda: M.moe_quant_i8(torch.zeros(5, 60), q, s), lambda: M.moe_quant_i8(f32(60, 5).T, q, s),
+                 lambda: M.moe_linear_i8(FakeLinear(7, 65), q, s, out, 0), lambda: M.moe_linear_i8(lin, q, f32(4), out, 0),
+                 lambda: M.moe_linear_i8(lin, q, s, f32(34), 0), lambda: M.moe_linear_i8(lin, q, s, out16, 0),
+                 lambda: M.moe_linear_i8(lin, i8(5, 128)[:, :64], s, out, 0)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    assert len(rec.calls) == n

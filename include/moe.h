@@ -211,6 +211,43 @@ moe_status moe_expert_forward(const moe_layer* L, const uint16_t* u, int32_t T, 
 size_t moe_workspace_size(const moe_layer* L, int32_t T, int32_t K);
 
 /*
+ * One whole layer for a few tokens (0 <= T <= MOE_LAYER_DECODE_MAX_TOKENS) in
+ * one cooperative launch: moe_rmsnorm_bf16 (where x is given), moe_route_topk
+ * and moe_expert_forward together.
+ *   u = x ? bf16(rmsnorm(x)) : u;  logits, idx: as moe_route_topk
+ *   executed[t] = exec_idx ? exec_idx[t] : idx[t]
+ *   w[t][k] = softmax over the K logits at executed[t]
+ *   out[t] = sum_k w[t][k] FFN_executed[t][k](u_t) + sigmoid(shared_gate . u_t) FFN_shared(u_t)
+ * x [T][H] fp32 or NULL; with x, u [T][H] bf16 is an output (or NULL), else the
+ *   input.  rmsnorm is rounded once to fp32 (of the exact quotient, the mean in
+ *   64 bits) and then to bf16.
+ * exec_idx [T][K] int32 or NULL: experts to execute in place of the router's own
+ *   top-K (predicted routing); a value outside [0,E) is clamped to 0 or E-1,
+ *   and an expert listed twice counts twice.
+ * logits [T][E] fp32 or NULL; idx [T][K] int32 (the router's own top-K, ordering
+ *   and ties as moe_route_topk; a NaN logit ranks below every number) and w [T][K]
+ *   fp32 are required outputs.
+ * out, out_mode as moe_expert_forward; out may be x itself (residual stream).
+ * All adapters of the layer are applied.  Accuracy: weights and u enter exactly
+ *   (u in any range: no MOE_ERR_RANGE for it), sums are fp32, hidden values carry
+ *   22 significant bits; a finite hidden value beyond fp16's range (|h| > 65504)
+ *   stores MOE_ERR_RANGE in err_word and leaves that token's output undefined.
+ * workspace: at least moe_layer_decode_workspace_size(L, T, K) bytes, 256-byte
+ *   aligned, contents on entry do not matter; calls that may overlap on the GPU
+ *   need workspaces of their own.  The launch needs every multiprocessor; two
+ *   calls on different streams run one after the other or wait for each other's
+ *   CTAs to leave, never in part.  Bounded waits as moe_expert_forward.
+ */
+#define MOE_LAYER_DECODE_MAX_TOKENS 32
+
+moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, float eps, int32_t T, int32_t K,
+                            const int32_t* exec_idx, float* logits, int32_t* idx, float* w, void* out, int32_t out_mode,
+                            void* workspace, size_t ws_bytes, int32_t* err_word, void* stream);
+
+/* Scratch bytes moe_layer_decode needs (host); 0 for a NULL layer, T < 0, T > MOE_LAYER_DECODE_MAX_TOKENS or K < 1. */
+size_t moe_layer_decode_workspace_size(const moe_layer* L, int32_t T, int32_t K);
+
+/*
  * Prerouter prediction (see moe_prerouter).  u [T][H] bf16; sel [T][K] int32
  * = experts executed at this layer, distinct within a row (each entry adds its
  * W1 column once, so distinct entries give the multi-hot product; a value

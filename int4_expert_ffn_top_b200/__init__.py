@@ -140,6 +140,34 @@ def moe_expert_forward(layer: DeviceLayer, u: torch.Tensor, K: int, idx: torch.T
                                         _stream(stream)))
 
 
+def moe_layer_decode_workspace_size(layer: DeviceLayer, T: int, K: int) -> int:
+    return lib().moe_layer_decode_workspace_size(ctypes.byref(layer.struct), T, K)
+
+
+def moe_layer_decode(layer: DeviceLayer, u: torch.Tensor | None, K: int, idx: torch.Tensor, w: torch.Tensor,
+                     out: torch.Tensor, out_mode: int, workspace: torch.Tensor, x: torch.Tensor | None = None,
+                     eps: float = 1e-6, exec_idx: torch.Tensor | None = None, logits: torch.Tensor | None = None,
+                     err_word: torch.Tensor | None = None, stream=None):
+    """The whole layer for up to 32 tokens in one launch: norm (of ``x``, if given), routing, experts, combine.
+
+    Without ``x``, ``u`` (bf16 ``[T, H]``) is the input; with ``x`` (fp32 ``[T, H]``) it receives bf16(rmsnorm(x)),
+    or is None.  ``exec_idx`` executes these experts instead of the router's own top-K, which ``idx`` receives.
+    """
+    fn, L = "moe_layer_decode", layer.struct
+    if x is not None:
+        T = _rows(fn, "x", x, L.H, F32)
+        pu = _arg(fn, "u", u, BF16_BITS, T * L.H, optional=True)
+    else:
+        T = _rows(fn, "u", u, L.H, BF16_BITS)
+        pu = _p(u)
+    args = (_arg(fn, "exec_idx", exec_idx, I32, T * K, optional=True),
+            _arg(fn, "logits", logits, F32, T * L.E, optional=True), _arg(fn, "idx", idx, I32, T * K),
+            _arg(fn, "w", w, F32, T * K), _arg(fn, "out", out, BF16_BITS if out_mode == OUT_BF16 else F32, T * L.H))
+    err = _arg(fn, "err_word", err_word, I32, 1, optional=True)
+    _check(fn, lib().moe_layer_decode(ctypes.byref(L), pu, _p(x), eps, T, K, *args, out_mode, *_ws(fn, workspace), err,
+                                      _stream(stream)))
+
+
 def moe_noalloc_scratch_bytes() -> int:
     return lib().moe_noalloc_scratch_bytes()
 

@@ -10,6 +10,7 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_RANGE = range(7)
 MOE_MAX_TOKENS = 524280  # most tokens one call takes
+MOE_LAYER_DECODE_MAX_TOKENS = 32  # most tokens of the whole-layer call
 
 
 class moe_qrows(ctypes.Structure):
@@ -56,6 +57,10 @@ SIGNATURES = {
     "moe_expert_forward": (c_int32, [POINTER(moe_layer), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
                                      c_int32, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "moe_workspace_size": (c_size_t, [POINTER(moe_layer), c_int32, c_int32]),
+    "moe_layer_decode": (c_int32, [POINTER(moe_layer), c_void_p, c_void_p, c_float, c_int32, c_int32, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_size_t, c_void_p,
+                                   c_void_p]),
+    "moe_layer_decode_workspace_size": (c_size_t, [POINTER(moe_layer), c_int32, c_int32]),
     "prerouter_predict": (c_int32, [POINTER(moe_prerouter), c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p,
                                     c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "prerouter_workspace_size": (c_size_t, [POINTER(moe_prerouter), c_int32]),

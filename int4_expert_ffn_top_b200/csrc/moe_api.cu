@@ -2,12 +2,14 @@
 // kernel launches on the caller's stream.  Nothing here allocates memory.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
 
 #include "../../include/moe.h"
 #include "dense_gemm.cuh"
+#include "layer_decode.cuh"
 #include "layer_kernels.cuh"
 #include "prefill_kernels.cuh"
 #include "stack_kernel.cuh"
@@ -1303,6 +1305,182 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
     }
   }
   return launch_status();
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------- one layer, few tokens, one launch
+namespace {
+
+struct LayerWs {
+  uint32_t* bar;
+  uint8_t* img;
+  float *us, *ic, *logits, *aux, *tgu, *tex;
+  uint16_t* h;
+  size_t bytes;
+};
+
+LayerWs carve_layer(void* base, const moe_layer* L, int T, int K) {
+  LayerWs w{};
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t o = off;
+    off = align_up(off + n, 256);
+    return base ? static_cast<char*>(base) + o : nullptr;
+  };
+  const size_t t = static_cast<size_t>(T), TK = t * K, r = L->r > 0 ? L->r : 0;
+  w.bar = reinterpret_cast<uint32_t*>(take(ld::kHeaderBytes));
+  w.img = reinterpret_cast<uint8_t*>(take(t * (2 * L->H + 16)));
+  w.us = reinterpret_cast<float*>(take(t * (L->H / 64) * 4));
+  w.ic = reinterpret_cast<float*>(take(t * 4));
+  w.logits = reinterpret_cast<float*>(take(t * L->E * 4));
+  w.aux = reinterpret_cast<float*>(take(t * (1 + 2 * r) * 4));
+  w.h = reinterpret_cast<uint16_t*>(take((TK + t) * 2 * L->I * 2));
+  w.tgu = reinterpret_cast<float*>(take(L->ex_lora_A_gu ? TK * 2 * r * 4 : 0));
+  w.tex = reinterpret_cast<float*>(take(L->ex_lora_A ? TK * r * 4 : 0));
+  w.bytes = off;
+  return w;
+}
+
+// Shared-memory plan for a grid of `grid` CTAs; false if the shape does not fit.
+bool plan_layer(ld::Smem* s, const moe_layer* L, int T, int K, int grid, bool smem_image) {
+  const int H = L->H, I = L->I, G = H / 64, RGU = qrow_bytes(H, 4), RDN = qrow_bytes(I, 4);
+  auto cdiv = [](int a, int b) { return (a + b - 1) / b; };
+  size_t o = 0;
+  auto put = [&](size_t n) {
+    const size_t at = align_up(o, 128);
+    o = at + n;
+    return static_cast<int>(at);
+  };
+  const int rows = cdiv(H, grid), nrt = cdiv(rows, ld::kDownRows), rt_rows = cdiv(rows, nrt);
+  const int nsp = cdiv(I, grid), nst = cdiv(nsp, 8);
+  const size_t y = static_cast<size_t>(T * K + T) * nrt * ld::kTileRows * 4;
+  s->img = smem_image ? put(static_cast<size_t>(T) * (2 * H + 16)) : 0;
+  s->us = put(static_cast<size_t>(T) * G * 4);
+  s->ic = put(T * 4);
+  s->scratch = put(y > 16384 ? y : 16384);
+  s->sraw = put(static_cast<size_t>(T) * 2 * nsp * 4);
+  s->sel = put(ld::kMaxSlots * 4);
+  s->w = put(ld::kMaxSlots * 4);
+  s->dist = put(ld::kMaxE * 4);
+  s->start = put((ld::kMaxE + 1) * 4);
+  s->slots = put(ld::kMaxSlots * 4);
+  s->els = put(ld::kMaxEls * 4);
+  s->gate = put(T * 4);
+  s->td = put(static_cast<size_t>(T) * ld::kMaxR * 4);
+  s->red = put(2 * ld::kWarps * 8);
+  s->bars = put((2 * 8 + 4) * (ld::kMaxStagesG + ld::kMaxStagesD) + 96);
+  s->ring = put(0);
+  s->sg = ld::padded_row(RGU);
+  s->stage_g = ld::kTileRows * s->sg;
+  s->sd = ld::padded_row(RDN);
+  s->stage_d = ld::kDownRows * s->sd;
+  const int room = 227 * 1024 - s->ring;
+  if (room <= 0) return false;
+  s->nsg = room / s->stage_g < ld::kMaxStagesG ? room / s->stage_g : ld::kMaxStagesG;
+  s->nsd = room / s->stage_d < ld::kMaxStagesD ? room / s->stage_d : ld::kMaxStagesD;
+  const int g_bytes = s->nsg * s->stage_g, d_bytes = s->nsd * s->stage_d;
+  s->total = s->ring + (g_bytes > d_bytes ? g_bytes : d_bytes);
+  return s->nsg > nst && s->nsg >= 2 && s->nsd >= 2 && rt_rows <= ld::kDownRows;
+}
+
+// Multiprocessors of the current device, with the kernel's shared memory allowed there; 0 on failure.
+int layer_grid() {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaFuncSetAttribute(ld::layer_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+            cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return 0;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_layer_decode_workspace_size(const moe_layer* L, int32_t T, int32_t K) {
+  if (!L || T < 0 || T > MOE_LAYER_DECODE_MAX_TOKENS || K < 1) return 0;
+  return carve_layer(nullptr, L, T, K).bytes;
+}
+
+moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, float eps, int32_t T, int32_t K,
+                            const int32_t* exec_idx, float* logits, int32_t* idx, float* w, void* out, int32_t out_mode,
+                            void* workspace, size_t ws_bytes, int32_t* err_word, void* stream) {
+  moe_status s = check_layer(L, T, K);
+  if (s != MOE_OK) return s;
+  if (T > MOE_LAYER_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  if (out_mode < 0 || out_mode > 2 || (x && !(eps >= 0.f))) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if ((!u && !x) || !idx || !w || !out || (u && !aligned(u, 16)) || (x && !aligned(x, 16))) return MOE_ERR_INVALID_ARG;
+  s = check_expert_weights(L);
+  if (s != MOE_OK) return s;
+  if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  const LayerWs ws = carve_layer(workspace, L, T, K);
+  if (ws_bytes < ws.bytes) return MOE_ERR_WORKSPACE;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = layer_grid();
+  if (grid < 64) return grid ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
+  ld::Args a{};
+  a.T = T;
+  a.K = K;
+  a.E = L->E;
+  a.H = L->H;
+  a.I = L->I;
+  while ((1 << a.logI) < L->I) ++a.logI;
+  a.r = L->r;
+  a.u = x ? nullptr : u;
+  a.x = x;
+  a.eps = eps;
+  a.u_out = x ? u : nullptr;
+  a.exec_idx = exec_idx;
+  a.logits = logits ? logits : ws.logits;
+  a.idx = idx;
+  a.w = w;
+  a.out = out;
+  a.out_mode = out_mode;
+  a.router = static_cast<const uint8_t*>(L->router.rows);
+  a.rbias = L->router_bias;
+  a.sgate = static_cast<const uint8_t*>(L->shared_gate.rows);
+  a.shared = static_cast<const uint8_t*>(L->shared_block);
+  if (L->r > 0) {
+    for (int p = 0; p < 3; ++p) {
+      a.shA[p] = L->sh_lora_A[p];
+      a.shB[p] = L->sh_lora_B[p];
+    }
+    a.exA = L->ex_lora_A;
+    a.exB = L->ex_lora_B;
+    a.exAgu = L->ex_lora_A_gu;
+    a.exBgu = L->ex_lora_B_gu;
+  }
+  a.lora_scale = L->lora_scale;
+  a.pool = static_cast<const uint8_t*>(L->pool);
+  a.stride = L->expert_stride;
+  a.bar = ws.bar;
+  a.img = ws.img;
+  a.us = ws.us;
+  a.ic = ws.ic;
+  a.aux = ws.aux;
+  a.h = ws.h;
+  a.tgu = ws.tgu;
+  a.tex = ws.tex;
+  a.err = err_word;
+  a.timeout_ns = kGemmTimeoutNs;
+  a.smem_image = T * L->H <= 32768;
+  a.shared_build = !a.smem_image || (x && T > 4);
+  if (!plan_layer(&a.sm, L, T, K, grid, a.smem_image)) return MOE_ERR_UNSUPPORTED;
+  if (cudaMemsetAsync(ws.bar, 0, ld::kHeaderBytes, st) != cudaSuccess) return MOE_ERR_CUDA;
+  void* args[] = {&a};
+  return cudaLaunchCooperativeKernel(reinterpret_cast<void*>(ld::layer_decode_kernel), dim3(grid), dim3(ld::kThreads),
+                                     args, a.sm.total, st) == cudaSuccess
+             ? MOE_OK
+             : (cudaGetLastError(), MOE_ERR_CUDA);
 }
 
 }  // extern "C"

@@ -8,6 +8,8 @@ codes, scales, biases (one contiguous span per expert).
 """
 from __future__ import annotations
 
+from types import SimpleNamespace
+
 import numpy as np
 import torch
 
@@ -121,6 +123,56 @@ class DeviceLayer:
         else:
             t["exAgu"] = t["exBgu"] = None
         self.struct = self._make_struct()
+
+    @classmethod
+    def from_tensors(cls, *, H: int, E: int, I: int, r: int, router: torch.Tensor, shared_gate: torch.Tensor,
+                     shared_block: torch.Tensor, pool: torch.Tensor, router_bias: torch.Tensor | None = None,
+                     shared_lora=None, routed_down_lora=None, routed_gate_up_lora=None,
+                     lora_scale: float = 1.0) -> "DeviceLayer":
+        """A layer over tensors that are on the device already, in the storage formats of ``include/moe.h``.
+
+        ``router`` uint8 ``[E, record]`` and ``shared_gate`` ``[1, record]`` (8-bit records), ``shared_block`` one
+        expert block, ``pool`` uint8 ``[E, stride]`` expert blocks, ``router_bias`` fp32 ``[E]``; adapters fp16:
+        ``shared_lora`` three ``(A, B)`` pairs (gate, up, down; or None each), ``routed_down_lora`` ``(A [E, r, I],
+        B [E, H, r])``, ``routed_gate_up_lora`` ``(A [E, 2, r, H], B [E, 2I, r])``.  Nothing is copied.
+        """
+        dev = pool.device
+
+        def take(name, t, dtype, shape, align=16):
+            if t is None:
+                return None
+            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev or \
+                    t.data_ptr() % align:
+                raise ValueError(f"DeviceLayer: {name} must be a contiguous {dtype} {list(shape)} tensor on {dev}, "
+                                 f"{align}-byte aligned")
+            return t
+
+        def pair(name, p, a_shape, b_shape):
+            if p is None or p[0] is None:
+                return None, None
+            return take(name + " A", p[0], torch.float16, a_shape), take(name + " B", p[1], torch.float16, b_shape)
+
+        if pool.dim() != 2 or pool.shape[1] < block_bytes(H, I) or pool.shape[1] % 256:
+            raise ValueError("DeviceLayer: pool must be [E, stride], stride a multiple of 256 that holds a block")
+        if shared_block.numel() < block_bytes(H, I):
+            raise ValueError("DeviceLayer: shared_block is smaller than an expert block")
+        self = cls.__new__(cls)
+        self.cfg = SimpleNamespace(H=H, E=E, I=I, I_s=I, r=r)
+        self.stride = pool.shape[1]
+        self.pool = take("pool", pool, torch.uint8, (E, self.stride), 256)
+        rec8 = qrow_bytes(H, 8)
+        t = self.t = {"router": take("router", router, torch.uint8, (E, rec8)),
+                      "router_bias": take("router_bias", router_bias, torch.float32, (E,), 4),
+                      "sgate": take("shared_gate", shared_gate, torch.uint8, (1, rec8)),
+                      "shared": take("shared_block", shared_block, torch.uint8, tuple(shared_block.shape))}
+        sh = shared_lora if shared_lora is not None else (None, None, None)
+        for i, (n_in, n_out) in enumerate(((H, I), (H, I), (I, H))):
+            t[f"A{i}"], t[f"B{i}"] = pair("shared_lora", sh[i], (r, n_in), (n_out, r))
+        t["exA"], t["exB"] = pair("routed_down_lora", routed_down_lora, (E, r, I), (E, H, r))
+        t["exAgu"], t["exBgu"] = pair("routed_gate_up_lora", routed_gate_up_lora, (E, 2, r, H), (E, 2 * I, r))
+        self.struct = self._make_struct()
+        self.struct.lora_scale = lora_scale
+        return self
 
     def fill_experts(self, experts: dict):
         if not experts:

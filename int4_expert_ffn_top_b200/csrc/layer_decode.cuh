@@ -30,34 +30,30 @@
 namespace moe {
 namespace ld {
 
-using tc::bar_arrive;
-using tc::bar_expect_tx;
-using tc::bar_init;
-using tc::bar_test;
 using tc::gtime;
 using tc::sa;
 
-constexpr int kWarps = 16;
-constexpr int kComp = 32 * kWarps;   // compute threads
-constexpr int kThreads = kComp + 32;  // and the warp that issues the weight copies
+constexpr int kWarps = 24;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxT = 32, kMaxK = 8, kMaxSlots = kMaxT * kMaxK, kMaxE = 256, kMaxR = 32;
-constexpr int kTileRows = 16;        // gate/up: 8 (gate, up) pairs
-constexpr int kDownRows = 15;        // down: row 15 of the MMA tile sums the hidden values
-constexpr int kSlotBlock = 4;        // down: slots per MMA (hi and lo columns)
-constexpr int kMaxStagesG = 16, kMaxStagesD = 32;
+constexpr int kDownRows = 15;  // down: row 15 of the MMA tile sums the hidden values
+constexpr int kSlotBlock = 4;  // down: slots per MMA (hi and lo columns)
 constexpr int kMaxEls = kMaxSlots + kMaxT / kSlotBlock;
+constexpr int kMaxSharedPairs = 16;  // pairs of the shared expert a CTA takes
 constexpr int kHeaderBytes = 256;
+constexpr int kUnitRow = 160, kUnitBytes = 16 * kUnitRow, kBuf = 2;  // see issue_unit
 
 enum Bar { B_IMAGE = 0, B_LOGITS = 1, B_EXGU = 2, B_HIDDEN = 3, B_EXDOWN = 4, kBars = 5 };
 
 struct Smem {  // byte offsets
-  int img, us, ic, scratch, sraw, sel, w, dist, start, slots, els, gate, td, red, bars, ring, total;
-  int sg, nsg, stage_g;  // gate/up: row stride, stages, stage bytes
-  int sd, nsd, stage_d;  // down
+  int img, us, ic, scratch, sraw, sel, w, dist, start, slots, els, gate, td, red, misc, ring, total;
 };
 
+struct Header;
+
 struct Args {
-  int T, K, E, H, I, logI, r;
+  int T, K, E, H, I, logI, logU, r;  // I = 2^logI, H / 256 = 2^logU
+  uint32_t gmul, kmul;  // 2^32 / grid and 2^16 / K, rounded up
   const uint16_t* u;  // bf16 [T][H], or null: the normed x
   const float* x;     // fp32 [T][H] to norm, or null
   float eps;
@@ -79,37 +75,24 @@ struct Args {
   int64_t stride;
   const uint16_t *exA, *exB, *exAgu, *exBgu;
   // workspace
-  uint32_t* bar;      // kBars counters, zero on entry
+  Header* bar;
   uint8_t* img;       // [T][2H + 16]
   float* us;          // [T][G]
   float* ic;          // [T]
-  float* aux;         // [1 + 2r][T]: shared gate logit, gate and up LoRA-A products
+  float* aux;         // [T][4 + 2r]: shared gate logit, (3 unused), gate and up LoRA-A products
   uint16_t* h;        // [T K + T][2][I]
   float* tgu;         // [T K][2][r]
   float* tex;         // [T K][r]
   int* err;
   long long timeout_ns;
-  int smem_image;     // the tokens' images are in shared memory
-  int shared_build;   // the images are formed once, by CTA t for token t, and passed through memory
+  int smem_image;     // every CTA forms the tokens' images in shared memory; else CTA t forms token t's, in img
   Smem sm;
 };
 
-// Row stride in shared memory: 32 or 96 bytes past a multiple of 128, so that the 8-byte reads of 4 rows x 32
-// bytes (one phase of a warp's fragment load) fall on different banks.
-__host__ __device__ constexpr int padded_row(int rec) {
-  int s = rec;
-  while (s % 128 != 32 && s % 128 != 96) s += 16;
-  return s;
-}
-
-// Barriers of the compute threads, of all threads, and of a team of warps.  Warps are reconverged first and the
-// barriers are the non-aligned form: lanes may come from loops of different trip counts.
 MOE_DEV void named_sync(int id, int threads) {
   __syncwarp();
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-MOE_DEV void cta_sync() { named_sync(15, kComp); }
-MOE_DEV void all_sync() { named_sync(14, kThreads); }
 MOE_DEV void team_sync(int team, int warps) {
   if (warps == 1)
     __syncwarp();
@@ -117,90 +100,99 @@ MOE_DEV void team_sync(int team, int warps) {
     named_sync(1 + team, 32 * warps);
 }
 
-MOE_DEV void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(sa(dst)),
-               "l"(src), "r"(bytes), "r"(sa(bar))
-               : "memory");
-}
-
 MOE_DEV void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-MOE_DEV float half_at(const uint8_t* p) { return half_bits_to_float(*reinterpret_cast<const uint16_t*>(p)); }
-
-// Bounded wait on an mbarrier phase; after a first failure of this CTA no wait blocks any more (the call's outputs
-// are undefined then, but every index read below stays in range).
-struct Waiter {
-  volatile int* failed;
-  int* err;
-  long long timeout_ns;
-  MOE_DEV void fail() const {
-    *failed = 1;
-    report(err, 5 /* MOE_ERR_TIMEOUT */);
-  }
-  MOE_DEV void wait(uint64_t* b, uint32_t parity, bool even_if_failed = false) const {
-    if (bar_test(b, parity)) return;
-    const long long end = gtime() + timeout_ns;
-    while (!bar_test(b, parity)) {
-      if (*failed && !even_if_failed) return;
-      if (gtime() > end) return fail();
-    }
-  }
-};
-
-// Wait for the copy that is number i in a ring of n stages.  Teams of warps take the ring's copies in turn, and a
-// parity tells a phase from its neighbours only, while the copy before this one in the stage is another team's and may
-// still be under way.  So the copying warp writes down which copy a stage holds next (`turn`) once the one before is
-// used up, and a consumer looks at the phase only after that.
-MOE_DEV void ring_open(uint32_t* turn, int i, int n) {
-  asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(sa(turn + i % n)), "r"(i) : "memory");
+// d = a b
+MOE_DEV void mma16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-MOE_DEV void ring_wait(const Waiter& wt, const uint32_t* turn, uint64_t* full, int i, int n) {
-  if (i >= n) {
-    const long long end = gtime() + wt.timeout_ns;
-    for (;;) {
-      int v;
-      asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(sa(turn + i % n)) : "memory");
-      if (v == i || *wt.failed) break;
-      if (gtime() > end) {
-        wt.fail();
-        break;
-      }
-    }
-  }
-  wt.wait(full + i % n, static_cast<uint32_t>(i / n) & 1u);
+
+MOE_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+MOE_DEV void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  __syncwarp();
 }
+MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+MOE_DEV float lo_half(uint32_t v) { return half_bits_to_float(static_cast<uint16_t>(v)); }
+MOE_DEV float hi_half(uint32_t v) { return half_bits_to_float(static_cast<uint16_t>(v >> 16)); }
 
 // ----------------------------------------------------------------------------- grid barrier
-// Each CTA adds one to the barrier's counter when its part is written; a CTA goes on when the counter has reached
-// the grid's size.  All CTAs are resident (cooperative launch).
-MOE_DEV void grid_arrive(const Args& a, int b) {
-  cta_sync();
-  if (threadIdx.x == 0) {
+// The header of the workspace: counters (one per barrier, one of CTAs that are through), between two marks that say
+// that the counters were left at zero.  The last CTA of a call leaves them so; where the marks do not hold (a new
+// workspace, or one that something else has written over) CTA 0 sets the header up before any CTA counts.
+struct Header {
+  unsigned long long mark0;
+  uint32_t count[kBars + 1];  // [kBars]: CTAs that are through with every barrier
+  unsigned long long mark1;
+};
+static_assert(sizeof(Header) <= kHeaderBytes, "header");
+
+__device__ __noinline__ void header_ready(Header* h, volatile int* failed, int* err, long long timeout_ns) {
+  const unsigned long long m0 = 0x6c617965725f6465ull ^ reinterpret_cast<unsigned long long>(h), m1 = ~m0;
+  volatile Header* v = h;
+  if (v->mark0 == m0 && v->mark1 == m1) return;
+  if (blockIdx.x == 0) {
+    for (int i = 0; i <= kBars; ++i) v->count[i] = 0;
     __threadfence();
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.bar + b) : "memory");
+    v->mark1 = m1;
+    v->mark0 = m0;
+    __threadfence();
+    return;
   }
+  const long long end = gtime() + timeout_ns;
+  while (v->mark0 != m0 || v->mark1 != m1) {
+    if (gtime() > end) {
+      *failed = 1;
+      report(err, 5 /* MOE_ERR_TIMEOUT */);
+      break;
+    }
+  }
+  __threadfence();
 }
 
-MOE_DEV void grid_wait(const Args& a, int b, const Waiter& wt) {
+// Each CTA adds one to a barrier's counter when its part is written and goes on when the counter has reached the
+// grid's size.  All CTAs are resident (cooperative launch).  After a wait that ran out no wait of this CTA blocks any
+// more: the call's outputs are undefined then, but every index read stays in range.
+// The release on the counter covers the whole CTA's writes (they come before it by the CTA's own barrier), and the
+// polls are plain reads with one acquire at the end: 1.1 us from arrival to departure on 148 CTAs, against 1.7 us with
+// a full fence on either side.
+MOE_DEV void grid_arrive(Header* h, int b) {
+  named_sync(15, kThreads);
+  if (threadIdx.x == 0)
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(h->count + b) : "memory");
+}
+
+__device__ __noinline__ void grid_wait(Header* h, int b, bool last, volatile int* failed, int* err,
+                                       long long timeout_ns) {
   if (threadIdx.x == 0) {
-    const long long end = gtime() + a.timeout_ns;
-    for (;;) {
-      uint32_t v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.bar + b) : "memory");
-      if (v >= gridDim.x || *wt.failed) break;
-      if (gtime() > end) {
-        wt.fail();
-        break;
+    const uint32_t* c = h->count + b;
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+    if (v < gridDim.x) {
+      const long long end = gtime() + timeout_ns;
+      for (;;) {
+        asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+        if (v >= gridDim.x || *failed) break;
+        if (gtime() > end) {
+          *failed = 1;
+          report(err, 5 /* MOE_ERR_TIMEOUT */);
+        }
       }
     }
-    __threadfence();
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+    if (last && atomicAdd(h->count + kBars, 1u) == gridDim.x - 1) {  // no CTA reads the counters any more
+      for (int i = 0; i <= kBars; ++i) *reinterpret_cast<volatile uint32_t*>(h->count + i) = 0;
+    }
   }
-  cta_sync();
+  named_sync(15, kThreads);
 }
 
 // ----------------------------------------------------------------------------- token images
@@ -217,12 +209,25 @@ MOE_DEV float max_bits(float a, float b) {  // non-negative floats by their bits
   return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
 
-MOE_DEV void load8(const Args& a, size_t at, float (&v)[8]) {
-  if (a.x) {
-    const float4 p = *reinterpret_cast<const float4*>(a.x + at), q = *reinterpret_cast<const float4*>(a.x + at + 4);
+// Eight values of a token as they are in memory: fp32, or bf16 pairs.
+template <bool F32>
+struct Raw8;
+template <>
+struct Raw8<true> {
+  float4 p, q;
+  MOE_DEV void load(const Args& a, size_t at) {
+    p = *reinterpret_cast<const float4*>(a.x + at);
+    q = *reinterpret_cast<const float4*>(a.x + at + 4);
+  }
+  MOE_DEV void get(float (&v)[8]) const {
     v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-  } else {
-    const uint4 p = *reinterpret_cast<const uint4*>(a.u + at);
+  }
+};
+template <>
+struct Raw8<false> {
+  uint4 p;
+  MOE_DEV void load(const Args& a, size_t at) { p = *reinterpret_cast<const uint4*>(a.u + at); }
+  MOE_DEV void get(float (&v)[8]) const {
     const uint32_t s[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -230,175 +235,267 @@ MOE_DEV void load8(const Args& a, size_t at, float (&v)[8]) {
       v[2 * i + 1] = __uint_as_float(s[i] & 0xffff0000u);
     }
   }
-}
+};
 
 // Token t's image by `warps` warps (this one is number wi): u scaled by a power of two c, fp16, pair order, odd pairs
-// / 16; per group 2^-24 sum of c u; 1/c.
-MOE_DEV void build_image(const Args& a, int t, int wi, int warps, int team, double* red, uint8_t* row, float* us,
-                         float* ic, bool write_u) {
-  const int lane = threadIdx.x & 31, nb = a.H / 8;
+// / 16; per group 2^-24 sum of c u; 1/c.  The squares are summed with their rounding errors (two fp32 numbers per lane), then in 64 bits: fp64 runs at a few lanes a
+// cycle, and a token's 2,048 squares in it cost more than the rest of the image.
+template <bool F32>
+__device__ __noinline__ void build_image(const Args& a, int t, int wi, int warps, int team, double* red, uint8_t* row,
+                                         float* us, float* ic, bool write_u) {
+  const int lane = threadIdx.x & 31, nb = a.H / 8, b0 = wi * 32 + lane, step = 32 * warps;
   const size_t base = static_cast<size_t>(t) * a.H;
-  float m = 0.f;
-  double ss = 0.0;
-  for (int b = wi * 32 + lane; b < nb; b += 32 * warps) {
-    float v[8];
-    load8(a, base + 8 * b, v);
+  constexpr int kChunk = 4;  // blocks whose loads are issued together
+  float m = 0.f, s = 0.f, e2 = 0.f;
+#pragma unroll 1
+  for (int c0 = b0; c0 < nb; c0 += kChunk * step) {
+    Raw8<F32> raw[kChunk];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_bits(m, fabsf(v[i]));
-    if (a.x) {
+    for (int i = 0; i < kChunk; ++i)
+      if (c0 + i * step < nb) raw[i].load(a, base + 8 * (c0 + i * step));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), ss);
-    }
+    for (int i = 0; i < kChunk; ++i)
+      if (c0 + i * step < nb) {
+        float v[8];
+        raw[i].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          m = max_bits(m, fabsf(v[j]));
+          if (F32) {
+            const float p = v[j] * v[j], sum = s + p, z = sum - s;
+            e2 += ((s - (sum - z)) + (p - z)) + fmaf(v[j], v[j], -p);
+            s = sum;
+          }
+        }
+      }
   }
   m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-  if (a.x) {
+  double ss = 0.0;
+  if (F32) {
+    ss = static_cast<double>(s) + static_cast<double>(e2);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   }
+  double* r = red + 2 * warps * team;
   if (warps > 1) {
-    double* r = red + 2 * warps * team;
     if (lane == 0) r[2 * wi] = ss, r[2 * wi + 1] = static_cast<double>(m);
     team_sync(team, warps);
     ss = 0.0;
+#pragma unroll 4
     for (int w = 0; w < warps; ++w) {
-      ss += r[2 * w];
+      if (F32) ss += r[2 * w];
       m = max_bits(m, static_cast<float>(r[2 * w + 1]));
     }
-    team_sync(team, warps);
   }
-  double rstd64 = 1.0;
   float rstd = 1.f;
-  if (a.x) {
+  double rstd64 = 1.0;
+  if (F32) {
+    if (m > 1e15f || m < 1e-15f) {  // squares that fp32 may not hold (uniform over the team): in 64 bits
+      ss = 0.0;
+#pragma unroll 1
+      for (int b = b0; b < nb; b += step)
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+          const double v = a.x[base + 8 * b + j];
+          ss = fma(v, v, ss);
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (warps > 1) {
+        team_sync(team, warps);
+        if (lane == 0) r[2 * wi] = ss;
+        team_sync(team, warps);
+        ss = 0.0;
+#pragma unroll 1
+        for (int w = 0; w < warps; ++w) ss += r[2 * w];
+      }
+    }
     rstd64 = 1.0 / sqrt(ss / a.H + static_cast<double>(a.eps));
     rstd = static_cast<float>(rstd64);
-    m *= rstd;
+    m = static_cast<float>(m * rstd64);
   }
   // c = 2^(9 - e) for m in [2^e, 2^(e+1)); 1 where m is zero or not finite
   const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
   const int ce = (m > 0.f && e < 128) ? min(max(9 - e, -126), 126) : 0;
   const float c = __uint_as_float(static_cast<uint32_t>(127 + ce) << 23);
   if (wi == 0 && lane == 0) *ic = __uint_as_float(static_cast<uint32_t>(127 - ce) << 23);
-  for (int b = wi * 32 + lane; b < nb; b += 32 * warps) {
-    float v[8];
-    load8(a, base + 8 * b, v);
-    if (a.x) {
-      uint32_t o[4];
+#pragma unroll 2
+  for (int b = b0; b < nb; b += step) {
+    {
+      float v[8];
+      Raw8<F32> raw;
+      raw.load(a, base + 8 * b);
+      raw.get(v);
+      if (F32) {
+        uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint16_t q = normed_bf16(v[i], rstd, rstd64);
-        v[i] = bf16_bits_to_float(q);
-        if (i & 1)
-          o[i >> 1] |= static_cast<uint32_t>(q) << 16;
-        else
-          o[i >> 1] = q;
+        for (int j = 0; j < 8; ++j) {
+          const uint16_t q = normed_bf16(v[j], rstd, rstd64);
+          v[j] = bf16_bits_to_float(q);
+          if (j & 1)
+            o[j >> 1] |= static_cast<uint32_t>(q) << 16;
+          else
+            o[j >> 1] = q;
+        }
+        if (write_u && a.u_out)
+          *reinterpret_cast<uint4*>(a.u_out + base + 8 * b) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      if (write_u && a.u_out) *reinterpret_cast<uint4*>(a.u_out + base + 8 * b) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-    float sum = 0.f;
+      float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] *= c;
-      sum += v[i];
-    }
-    uint32_t p[4];
+      for (int j = 0; j < 8; ++j) {
+        v[j] *= c;
+        sum += v[j];
+      }
+      uint32_t p[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float f = (j & 1) ? 0.0625f : 1.f;
-      p[j] = h2_bits(__floats2half2_rn(v[j] * f, v[j + 4] * f));
+      for (int j = 0; j < 4; ++j) {
+        const float f = (j & 1) ? 0.0625f : 1.f;
+        p[j] = h2_bits(__floats2half2_rn(v[j] * f, v[j + 4] * f));
+      }
+      *reinterpret_cast<uint4*>(row + 16 * b) = make_uint4(p[0], p[1], p[2], p[3]);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      if ((b & 7) == 0) us[b >> 3] = sum * 0x1p-24f;
     }
-    *reinterpret_cast<uint4*>(row + 16 * b) = make_uint4(p[0], p[1], p[2], p[3]);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-    if ((b & 7) == 0) us[b >> 3] = sum * 0x1p-24f;
   }
 }
 
-// Two B registers quads of a lane's 8-blocks 2 tig and 2 tig + 1 of group gi (image rows, shared or global memory).
-struct BFrag {
+// ----------------------------------------------------------------------------- int4 units
+// The unit of weight traffic and of work: 16 rows x 4 groups (2 where a row has only 2), brought by one warp into its
+// own buffers with cp.async (128 code bytes a row, then its 4 scales and 4 biases; row stride 160 bytes, 32 past a
+// multiple of 128, so that the 8-byte fragment reads of 4 rows fall on different banks) and used by that warp alone:
+// no barrier is needed between copy and use, and each of 24 warps has kBuf units of 2.3 KB, one in use and the rest in flight.
+// Row m of a unit is record (m % 8) * step_lo + (m / 8) * step_hi: gate rows over up rows for gate/up (2, 1), rows in
+// order for down (1, 8).
+struct UnitPlan {  // a lane's places: bytes from the unit's first record (its chunk of row lane/8; its scales)
+  uint32_t c0, c4, c8, c12, s;
+  uint32_t dst, dst_s;
+  bool on, four;
+  MOE_DEV void make(int rec, int G, int step_lo, int step_hi) {
+    const int lane = threadIdx.x & 31, q = lane >> 3, ch = lane & 7, m = lane >> 1;
+    four = G >= 4;
+    on = ch < (four ? 8 : 2 * G);
+    c0 = q * step_lo * rec + 16 * ch;
+    c4 = c0 + 4 * step_lo * rec;
+    c8 = c0 + step_hi * rec;
+    c12 = c4 + step_hi * rec;
+    s = ((m & 7) * step_lo + (m >> 3) * step_hi) * rec + G * 32 + 2 * G * (lane & 1);
+    dst = q * kUnitRow + 16 * ch;
+    dst_s = m * kUnitRow + 128 + 8 * (lane & 1);
+  }
+};
+
+// Copy a unit: lo and hi rows of each half exist.  base: the first record plus 128 bytes a unit; sbase: plus 8 bytes a
+// unit.
+MOE_DEV void issue_unit(uint32_t buf, const UnitPlan& p, const uint8_t* base, const uint8_t* sbase, int lo, int hi) {
+  const int lane = threadIdx.x & 31, q = lane >> 3, m = lane >> 1;
+  auto cp16 = [](uint32_t d, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  };
+  const uint32_t d = buf + p.dst;
+  if (p.on) {
+    if (q < lo) cp16(d, base + p.c0);
+    if (q + 4 < lo) cp16(d + 4 * kUnitRow, base + p.c4);
+    if (q < hi) cp16(d + 8 * kUnitRow, base + p.c8);
+    if (q + 4 < hi) cp16(d + 12 * kUnitRow, base + p.c12);
+  }
+  if ((m & 7) < (m < 8 ? lo : hi)) {
+    if (p.four)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(buf + p.dst_s), "l"(sbase + p.s) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(buf + p.dst_s), "l"(sbase + p.s) : "memory");
+  }
+}
+
+struct Frag {  // the N side of one group: a lane's 8-blocks 2 tig and 2 tig + 1
   uint4 x, y;
 };
-MOE_DEV BFrag b_frag(const uint8_t* row, int gi, int tig) {
-  const uint4* p = reinterpret_cast<const uint4*>(row + gi * 128 + tig * 32);
+
+MOE_DEV Frag load_frag(const uint8_t* col, int i) {
+  const uint4* p = reinterpret_cast<const uint4*>(col + i * 128 + (threadIdx.x & 3) * 32);
   return {p[0], p[1]};
 }
-MOE_DEV BFrag b_frag_l2(const uint8_t* row, int gi, int tig) {
-  const uint4* p = reinterpret_cast<const uint4*>(row + gi * 128 + tig * 32);
-  return {__ldcg(p), __ldcg(p + 1)};
-}
 
-// ----------------------------------------------------------------------------- int4 rows: gate/up
-// acc += rows g and g + 8 of the stage over groups [g0, g1) times NB column blocks of 8.
-template <int NB>
-MOE_DEV void int4_tile(const uint8_t* stage, int sg, int code_bytes, int G, int g0, int g1, const uint8_t* const (&col)[NB],
-                       const float* const (&ua)[NB], const float* const (&ub)[NB], float (&acc)[NB][4]) {
+// acc += one unit of gate/up rows times 8 columns, two groups at a time (four would take half as many warps again in
+// registers).
+MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* col, const float* ua, const float* ub, float (&acc)[4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const uint8_t* ra = stage + g * sg;
-  const uint8_t* rb = ra + 8 * sg;
-#pragma unroll 2
-  for (int gi = g0; gi < g1; ++gi) {
-    const uint2 wa = *reinterpret_cast<const uint2*>(ra + gi * 32 + tig * 8);
-    const uint2 wb = *reinterpret_cast<const uint2*>(rb + gi * 32 + tig * 8);
-    const float s0 = half_at(ra + code_bytes + 2 * gi), b0 = half_at(ra + code_bytes + 2 * (G + gi));
-    const float s1 = half_at(rb + code_bytes + 2 * gi), b1 = half_at(rb + code_bytes + 2 * (G + gi));
-    BFrag f[NB];
+  const uint8_t* ra = buf + g * kUnitRow;
+  const uint8_t* rb = ra + 8 * kUnitRow;
+  const uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) f[n] = b_frag(col[n], gi, tig);
-    const uint32_t wa8 = wa.x >> 8, wb8 = wb.x >> 8, va8 = wa.y >> 8, vb8 = wb.y >> 8;
-    const uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
+  for (int h = 0; h < 2; ++h) {
+    float d[2][4];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma16(d, wa.x & lo, wb.x & lo, wa.x & hi, wb.x & hi, f[n].x.x, f[n].x.y);
-      mma16(d, wa8 & lo, wb8 & lo, wa8 & hi, wb8 & hi, f[n].x.z, f[n].x.w);
-      mma16(d, wa.y & lo, wb.y & lo, wa.y & hi, wb.y & hi, f[n].y.x, f[n].y.y);
-      mma16(d, va8 & lo, vb8 & lo, va8 & hi, vb8 & hi, f[n].y.z, f[n].y.w);
-      const float u0 = ua[n][gi], u1 = ub[n][gi];
-      acc[n][0] = fmaf(b0, u0, fmaf(s0, d[0], acc[n][0]));
-      acc[n][1] = fmaf(b0, u1, fmaf(s0, d[1], acc[n][1]));
-      acc[n][2] = fmaf(b1, u0, fmaf(s1, d[2], acc[n][2]));
-      acc[n][3] = fmaf(b1, u1, fmaf(s1, d[3], acc[n][3]));
+    for (int i = 0; i < 2; ++i) {
+      const Frag f = load_frag(col, 2 * h + i);
+      const uint2 wa = *reinterpret_cast<const uint2*>(ra + (2 * h + i) * 32 + tig * 8);
+      const uint2 wb = *reinterpret_cast<const uint2*>(rb + (2 * h + i) * 32 + tig * 8);
+      const uint32_t wa8 = wa.x >> 8, wb8 = wb.x >> 8, va8 = wa.y >> 8, vb8 = wb.y >> 8;
+      mma16_0(d[i], wa.x & lo, wb.x & lo, wa.x & hi, wb.x & hi, f.x.x, f.x.y);
+      mma16(d[i], wa8 & lo, wb8 & lo, wa8 & hi, wb8 & hi, f.x.z, f.x.w);
+      mma16(d[i], wa.y & lo, wb.y & lo, wa.y & hi, wb.y & hi, f.y.x, f.y.y);
+      mma16(d[i], va8 & lo, vb8 & lo, va8 & hi, vb8 & hi, f.y.z, f.y.w);
+    }
+    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(ra + 128 + 4 * h), b0 = *reinterpret_cast<const uint32_t*>(ra + 136 + 4 * h);
+    const uint32_t s1 = *reinterpret_cast<const uint32_t*>(rb + 128 + 4 * h), b1 = *reinterpret_cast<const uint32_t*>(rb + 136 + 4 * h);
+    const float2 u = *reinterpret_cast<const float2*>(ua + 2 * h), v = *reinterpret_cast<const float2*>(ub + 2 * h);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float p = i ? hi_half(s0) : lo_half(s0), q = i ? hi_half(b0) : lo_half(b0);
+      const float r = i ? hi_half(s1) : lo_half(s1), t = i ? hi_half(b1) : lo_half(b1), ui = i ? u.y : u.x, vi = i ? v.y : v.x;
+      acc[0] = fmaf(q, ui, fmaf(p, d[i][0], acc[0]));
+      acc[1] = fmaf(q, vi, fmaf(p, d[i][1], acc[1]));
+      acc[2] = fmaf(t, ui, fmaf(r, d[i][2], acc[2]));
+      acc[3] = fmaf(t, vi, fmaf(r, d[i][3], acc[3]));
     }
   }
 }
 
-// One (tile, block of 8 NB columns) by a team of W warps: partial sums of the warps' groups to part[w][16][8 NB].
-// token(c): token of column c.
-template <int NB, class TokenFn>
-MOE_DEV void gate_up_block(const Args& a, const uint8_t* img, const float* us, const uint8_t* stage, int wi, int W,
-                           float* part, TokenFn token) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3, G = a.H / 64, ldu = 2 * a.H + 16;
-  const uint8_t* col[NB];
-  const float *ua[NB], *ub[NB];
-  float acc[NB][4];
+// acc += one unit of down rows (15 of them; row 15 sums the columns) times the 8 columns (hi and lo of 4 slots).
+// Codes enter as code 2^-22 (and 16 times that).  The MMA aligns its products by their exponents, and a subnormal
+// counts with the smallest one, so two more of the mantissa's bits in use keep two more of h's 11 in the sum (u's 8 fit
+// either way): the result is off by 7e-7 of its size instead of 3e-6.
+MOE_DEV void down_unit(const uint8_t* buf, const uint8_t* col, bool whole, float (&acc)[4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+  const bool ones = g == 7;
+  const uint8_t* ra = buf + g * kUnitRow;
+  const uint8_t* rb = ones ? ra : ra + 8 * kUnitRow;
+  const uint32_t lo = 0x003C003Cu, hi = 0x03C003C0u, one = 0x3C003C00u, sixteen = 0x4C004C00u;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    col[n] = img + static_cast<size_t>(token(8 * n + g)) * ldu;
-    ua[n] = us + token(8 * n + 2 * tig) * G;
-    ub[n] = us + token(8 * n + 2 * tig + 1) * G;
+  for (int h = 0; h < 2; ++h) {
+    if (h && !whole) break;  // a row of two groups
+    float d[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-  }
-  int4_tile<NB>(stage, a.sm.sg, a.H / 2, G, wi * G / W, (wi + 1) * G / W, col, ua, ub, acc);
-  float* p = part + wi * (16 * 8 * NB);
+    for (int i = 0; i < 2; ++i) {
+      const Frag f = load_frag(col, 2 * h + i);
+      const uint2 wa = *reinterpret_cast<const uint2*>(ra + (2 * h + i) * 32 + tig * 8);
+      const uint2 wb = *reinterpret_cast<const uint2*>(rb + (2 * h + i) * 32 + tig * 8);
+      const uint32_t p0 = wa.x << 2, p1 = wa.x >> 6, p2 = wa.y << 2, p3 = wa.y >> 6;
+      const uint32_t q0 = wb.x << 2, q1 = wb.x >> 6, q2 = wb.y << 2, q3 = wb.y >> 6;
+      mma16_0(d[i], p0 & lo, ones ? one : q0 & lo, p0 & hi, ones ? sixteen : q0 & hi, f.x.x, f.x.y);
+      mma16(d[i], p1 & lo, ones ? one : q1 & lo, p1 & hi, ones ? sixteen : q1 & hi, f.x.z, f.x.w);
+      mma16(d[i], p2 & lo, ones ? one : q2 & lo, p2 & hi, ones ? sixteen : q2 & hi, f.y.x, f.y.y);
+      mma16(d[i], p3 & lo, ones ? one : q3 & lo, p3 & hi, ones ? sixteen : q3 & hi, f.y.z, f.y.w);
+    }
+    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(ra + 128 + 4 * h), b0 = *reinterpret_cast<const uint32_t*>(ra + 136 + 4 * h);
+    const uint32_t s1 = *reinterpret_cast<const uint32_t*>(rb + 128 + 4 * h), b1 = *reinterpret_cast<const uint32_t*>(rb + 136 + 4 * h);
 #pragma unroll
-  for (int n = 0; n < NB; ++n) {
-    *reinterpret_cast<float2*>(p + g * (8 * NB) + 8 * n + 2 * tig) = make_float2(acc[n][0], acc[n][1]);
-    *reinterpret_cast<float2*>(p + (g + 8) * (8 * NB) + 8 * n + 2 * tig) = make_float2(acc[n][2], acc[n][3]);
+    for (int i = 0; i < 2; ++i) {
+      const float u = __shfl_sync(0xffffffffu, d[i][2], 28 + tig) * 0x1p-22f;
+      const float v = __shfl_sync(0xffffffffu, d[i][3], 28 + tig) * 0x1p-22f;
+      const float p = i ? hi_half(s0) : lo_half(s0), q = i ? hi_half(b0) : lo_half(b0);
+      const float r = i ? hi_half(s1) : lo_half(s1), t = i ? hi_half(b1) : lo_half(b1);
+      acc[0] = fmaf(q, u, fmaf(p, d[i][0], acc[0]));
+      acc[1] = fmaf(q, v, fmaf(p, d[i][1], acc[1]));
+      acc[2] = fmaf(t, u, fmaf(r, d[i][2], acc[2]));
+      acc[3] = fmaf(t, v, fmaf(r, d[i][3], acc[3]));
+    }
   }
 }
 
-// (a, b) of pair pr, column c: the warps' partial sums in order, scaled back.
-template <int NB>
-MOE_DEV float2 pair_sum(const float* part, int W, int pr, int c) {
-  float x = 0.f, y = 0.f;
-  for (int w = 0; w < W; ++w) {
-    x += part[w * (16 * 8 * NB) + (2 * pr) * (8 * NB) + c];
-    y += part[w * (16 * 8 * NB) + (2 * pr + 1) * (8 * NB) + c];
-  }
-  return make_float2(x * 0x1p24f, y * 0x1p24f);
-}
-
+// ----------------------------------------------------------------------------- hidden values, adapters
 // Hidden value j of row `row` of the hidden buffer, as hi and lo.
 MOE_DEV void store_h(const Args& a, int row, int j, float x, float y) {
   const float v = silu(x) * y;
@@ -411,307 +508,308 @@ MOE_DEV void store_h(const Args& a, int row, int j, float x, float y) {
   p[a.I] = __half_as_ushort(lo);
 }
 
-MOE_DEV float dot_r(const uint16_t* B, const float* t, int r) {
+// sum_i B[i] t[i], r a multiple of 8, both 16-byte aligned.
+__device__ __noinline__ float dot_r(const uint16_t* B, const float* t, int r) {
   float v = 0.f;
-  for (int i = 0; i < r; ++i) v = fmaf(half_bits_to_float(B[i]), __ldcg(t + i), v);
+#pragma unroll 2
+  for (int i = 0; i < r; i += 8) {
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(B + i));
+    const float4 p = __ldcg(reinterpret_cast<const float4*>(t + i)), q = __ldcg(reinterpret_cast<const float4*>(t + i + 4));
+    v = fmaf(lo_half(b.x), p.x, v);
+    v = fmaf(hi_half(b.x), p.y, v);
+    v = fmaf(lo_half(b.y), p.z, v);
+    v = fmaf(hi_half(b.y), p.w, v);
+    v = fmaf(lo_half(b.z), q.x, v);
+    v = fmaf(hi_half(b.z), q.y, v);
+    v = fmaf(lo_half(b.w), q.z, v);
+    v = fmaf(hi_half(b.w), q.w, v);
+  }
   return v;
 }
 
-// ----------------------------------------------------------------------------- fp16 rows (LoRA A)
-// even/odd accumulators of rows g and g + 8 (row pointers, in halves) over groups [g0, g1) times one column block.
-template <bool L2, class Col>
-MOE_DEV void f16_rows(const uint16_t* ra, const uint16_t* rb, int g0, int g1, Col col, float (&ev)[4], float (&od)[4]) {
+// Rows g and g + 8 of an fp16 matrix (row pointers) over groups [g0, g1) times 8 columns of image layout: ev + 16 od.
+MOE_DEV void f16_rows(const uint16_t* ra, const uint16_t* rb, int g0, int g1, const uint8_t* col, float (&v)[4]) {
   const int tig = threadIdx.x & 3;
+  float ev[4] = {0.f, 0.f, 0.f, 0.f}, od[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
   for (int gi = g0; gi < g1; ++gi) {
-    const BFrag f = L2 ? b_frag_l2(col, gi, tig) : b_frag(col, gi, tig);
-    const uint4* pa = reinterpret_cast<const uint4*>(ra + gi * 64 + tig * 16);
-    const uint4* pb = reinterpret_cast<const uint4*>(rb + gi * 64 + tig * 16);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint4 x = __ldg(pa + h), y = __ldg(pb + h), b = h ? f.y : f.x;
+      const uint4* bp = reinterpret_cast<const uint4*>(col + gi * 128 + tig * 32) + h;
+      const uint4 b = *bp;
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(ra + gi * 64 + tig * 16) + h);
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(rb + gi * 64 + tig * 16) + h);
       mma16(ev, prmt(x.x, x.z, 0x5410), prmt(y.x, y.z, 0x5410), prmt(x.y, x.w, 0x5410), prmt(y.y, y.w, 0x5410), b.x, b.z);
       mma16(od, prmt(x.x, x.z, 0x7632), prmt(y.x, y.z, 0x7632), prmt(x.y, x.w, 0x7632), prmt(y.y, y.w, 0x7632), b.y, b.w);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = fmaf(16.f, od[i], ev[i]);
 }
 
-// ----------------------------------------------------------------------------- the kernel
-struct Tile {  // 8 or fewer (gate, up) pairs of one chosen expert
-  int d, p0, n;
-};
-MOE_DEV Tile next_tile(int pos, int hi, int logI) {
-  const int d = pos >> logI, p0 = pos & ((1 << logI) - 1);
-  const int end = min(hi, (d + 1) << logI);
-  return {d, p0, min(kTileRows / 2, end - pos)};
-}
-
-MOE_DEV uint32_t fparity(int i, int n) { return static_cast<uint32_t>(i / n) & 1u; }
-
-// Lanes of the copy warp bring `rows` records of `rec` bytes to `dst` (row stride `ld`).
-MOE_DEV void copy_rows(uint8_t* dst, int ld, const uint8_t* src, int rec, int rows, uint64_t* bar) {
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) bar_expect_tx(bar, static_cast<uint32_t>(rec * rows));
-  __syncwarp();
-  if (ld == rec) {
-    if (lane == 0) bulk_copy(dst, src, static_cast<uint32_t>(rec * rows), bar);
-  } else if (lane < rows) {
-    bulk_copy(dst + lane * ld, src + static_cast<size_t>(lane) * rec, static_cast<uint32_t>(rec), bar);
+// ----------------------------------------------------------------------------- top-K and gating of one token (a warp)
+__device__ __noinline__ void route_token(const Args& a, int t, int* sel, float* sw, uint32_t* mask) {
+  const int lane = threadIdx.x & 31, K = a.K;
+  const float* lg = a.logits + static_cast<size_t>(t) * a.E;
+  uint32_t key[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane + 32 * i;
+    uint32_t k = 0;
+    if (e < a.E) {
+      const float v = __ldcg(lg + e);
+      const uint32_t b = __float_as_uint(v);
+      k = v != v ? 1u : b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);  // order of the floats; NaN last
+    }
+    key[i] = k;
+  }
+  int my_e = 0;
+#pragma unroll 1
+  for (int k = 0; k < K; ++k) {
+    uint32_t best = key[0];
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (key[i] > best) best = key[i], bi = i;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int e =
+        static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffu));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e == lane + 32 * i) key[i] = 0;
+    if (lane == k) my_e = min(e, a.E - 1);
+  }
+  const bool write = blockIdx.x == 0;
+  if (lane < K && write) a.idx[t * K + lane] = my_e;
+  if (a.exec_idx && lane < K) my_e = min(max(a.exec_idx[t * K + lane], 0), a.E - 1);
+  const float l = lane < K ? __ldcg(lg + my_e) : -INFINITY;
+  float mx = l;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float ex = lane < K ? expf(l - mx) : 0.f;
+  float den = ex;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (lane < K) {
+    const int s = t * K + lane;
+    sel[s] = my_e;
+    sw[s] = ex / den;
+    atomicOr(mask + my_e * 8 + (s >> 5), 1u << (s & 31));
+    if (write) a.w[s] = ex / den;
   }
 }
 
+// Where the part of CTA c of n things split over the grid begins: c n / grid, with gmul = 2^32 / grid rounded up.
+// (Neighbours agree on the border whatever the rounding; at c = grid it is n for every n up to 2^19.)
+MOE_DEV int share(int c, int n, uint32_t gmul) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(c) * static_cast<uint32_t>(n)) * gmul) >> 32);
+}
+
+// ----------------------------------------------------------------------------- the kernel
 __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) uint8_t sm[];
   const Smem& S = a.sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tig = lane & 3;
   const int cta = blockIdx.x, grid = gridDim.x;
-  const int T = a.T, K = a.K, TK = T * K, G = a.H / 64, G2 = a.I / 64, ldu = 2 * a.H + 16, r = a.r;
-  uint64_t* full_g = reinterpret_cast<uint64_t*>(sm + S.bars);
-  uint64_t* empty_g = full_g + kMaxStagesG;
-  uint64_t* full_d = empty_g + kMaxStagesG;
-  uint64_t* empty_d = full_d + kMaxStagesD;
-  int* misc = reinterpret_cast<int*>(empty_d + kMaxStagesD);  // [0] failed, [1] distinct experts, [2] down elements
-  uint32_t* turn_g = reinterpret_cast<uint32_t*>(misc + 24);
-  uint32_t* turn_d = turn_g + kMaxStagesG;
-  const Waiter wt{misc, a.err, a.timeout_ns};
+  const int T = a.T, K = a.K, TK = T * K, G = a.H / 64, ldu = 2 * a.H + 16, r = a.r;
+  const int U = G / 4, G2 = a.I / 64, U2 = G2 < 4 ? 1 : G2 / 4;
+  int* misc = reinterpret_cast<int*>(sm + S.misc);  // [0] failed, [1] distinct experts, [2] down elements, [4..19] sums
   int* sel = reinterpret_cast<int*>(sm + S.sel);
   float* sw = reinterpret_cast<float*>(sm + S.w);
   int* dist = reinterpret_cast<int*>(sm + S.dist);
   int* start = reinterpret_cast<int*>(sm + S.start);
-  int* slots = reinterpret_cast<int*>(sm + S.slots);
+  int* slots = reinterpret_cast<int*>(sm + S.slots);  // slot | token << 16
   int* els = reinterpret_cast<int*>(sm + S.els);
   float* scratch = reinterpret_cast<float*>(sm + S.scratch);
   float* sraw = reinterpret_cast<float*>(sm + S.sraw);
-  uint8_t* ring = sm + S.ring;
+  uint8_t* ring = sm + S.ring + warp * (kBuf * kUnitBytes);
 
-  // this CTA's shares: pairs of the shared expert, rows of the down projections
-  const int sp0 = cta * a.I / grid, sp1 = (cta + 1) * a.I / grid, nsp = sp1 - sp0;
-  const int nst = (nsp + 7) / 8;  // shared tiles
-  const int dr0 = cta * a.H / grid, ndr = (cta + 1) * a.H / grid - dr0;
-  const int nrt = (ndr + kDownRows - 1) / kDownRows, rt_rows = nrt ? (ndr + nrt - 1) / nrt : 0;
-  const int RGU = qrow_bytes(a.H, 4), RDN = qrow_bytes(a.I, 4);
+  // this CTA's shares: pairs of the shared expert, rows of the down projections, rows over all tokens
+  const int sp0 = share(cta, a.I, a.gmul), nsp = share(cta + 1, a.I, a.gmul) - sp0, nst = (nsp + 7) / 8;
+  const int dr0 = share(cta, a.H, a.gmul), ndr = share(cta + 1, a.H, a.gmul) - dr0;
+  const int nrt = (ndr > 0) + (ndr > kDownRows), rt_rows = nrt > 1 ? (ndr + 1) / 2 : ndr;  // row tiles, rows of one
+  const int RGU = qrow_bytes(a.H, 4), RDN = qrow_bytes(a.I, 4), R8 = qrow_bytes(a.H, 8);
   const size_t dn_off = static_cast<size_t>(2 * a.I) * RGU;
   const int sh_blocks = (T + kSlotBlock - 1) / kSlotBlock;
+  const int nA = (a.shA[0] ? r : 0) + (a.shA[1] ? r : 0);
+  const int nrows = a.E + 1 + nA, r0 = share(cta, nrows, a.gmul), r1 = share(cta + 1, nrows, a.gmul);
+  const int n8 = max(0, min(r1, a.E + 1) - r0);  // 8-bit rows r0 .. r0 + n8 - 1, then fp16 rows
+  const int nblk = (T + 7) / 8;
 
-  if (tid == 0) {
-    for (int i = 0; i < kMaxStagesG; ++i) bar_init(full_g + i, 1), bar_init(empty_g + i, 1);
-    for (int i = 0; i < kMaxStagesD; ++i) bar_init(full_d + i, 1), bar_init(empty_d + i, 1);
-    for (int i = 0; i < kMaxStagesG + kMaxStagesD; ++i) turn_g[i] = 0;
-    misc[0] = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // --------------------------------------------------------------------------- weights that no token decides
+  // The first shared tile's units: unit warp % U for token blocks warp / U, + sh_n, ...
+  const uint32_t ring32 = sa(ring);
+  const int sh_ways = max(1, min(nblk, kWarps >> a.logU));
+  UnitPlan plan;
+  plan.make(RGU, G, 2, 1);
+  {
+    const uint8_t* src = a.shared + static_cast<size_t>(2 * sp0) * RGU;
+    const int u = warp & (U - 1), n = min(8, nsp);
+    if (nst > 0 && warp < U * sh_ways) issue_unit(ring32, plan, src + 128 * u, src + 8 * u, n, n);
+    cp_commit();
   }
-  __syncthreads();
-
-  if (warp == kWarps) {
-    // ------------------------------------------------------------------------- weight copies
-    for (int i = 0; i < nst; ++i)
-      copy_rows(ring + i * S.stage_g, S.sg, a.shared + static_cast<size_t>(2 * (sp0 + 8 * i)) * RGU, RGU,
-                2 * min(8, nsp - 8 * i), full_g + i);
-    all_sync();  // the expert list stands
-    const int D = misc[1], nel = misc[2];
-    const int lo = static_cast<int>(static_cast<long long>(cta) * (D << a.logI) / grid);
-    const int hi = static_cast<int>(static_cast<long long>(cta + 1) * (D << a.logI) / grid);
-    int n = nst;
-    for (int pos = lo; pos < hi; ++n) {
-      const Tile t = next_tile(pos, hi, a.logI);
-      const int s = n % S.nsg;
-      if (n >= S.nsg) {
-        wt.wait(empty_g + s, fparity(n - S.nsg, S.nsg));
-        if (lane == 0) ring_open(turn_g, n, S.nsg);
+  const int g0 = warp * G / kWarps, g1 = (warp + 1) * G / kWarps;  // groups of the rows over all tokens: up to 3
+  uint4 q8[3];
+  uint32_t sb8[3];  // scale and bias
+  if (n8 > 0) {
+    const int row = r0 + min(g, n8 - 1);
+    const uint8_t* rec = row < a.E ? a.router + static_cast<size_t>(row) * R8 : a.sgate;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (g0 + i < g1) {
+        q8[i] = __ldg(reinterpret_cast<const uint4*>(rec + (g0 + i) * 64 + tig * 16));
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + a.H) + g0 + i;
+        sb8[i] = __ldg(p) | static_cast<uint32_t>(__ldg(p + G)) << 16;
       }
-      copy_rows(ring + s * S.stage_g, S.sg, a.pool + dist[t.d] * a.stride + static_cast<size_t>(2 * t.p0) * RGU, RGU,
-                2 * t.n, full_g + s);
-      pos += t.n;
-    }
-    for (int i = max(0, n - S.nsg); i < n; ++i) wt.wait(empty_g + i % S.nsg, fparity(i, S.nsg));  // the ring is free
-    const int total = nrt * nel;
-    for (int i = 0; i < total; ++i) {
-      const int rt = i / nel, el = els[i - rt * nel], d = el & 511, s = i % S.nsd;
-      const uint8_t* block = d == 511 ? a.shared : a.pool + dist[d] * a.stride;
-      if (i >= S.nsd) {
-        wt.wait(empty_d + s, fparity(i - S.nsd, S.nsd));
-        if (lane == 0) ring_open(turn_d, i, S.nsd);
-      }
-      copy_rows(ring + s * S.stage_d, S.sd, block + dn_off + static_cast<size_t>(dr0 + rt * rt_rows) * RDN, RDN,
-                min(rt_rows, ndr - rt * rt_rows), full_d + s);
-    }
-    // no copy may be in flight when the CTA leaves
-    for (int i = max(0, n - S.nsg); i < n; ++i) wt.wait(full_g + i % S.nsg, fparity(i, S.nsg), true);
-    for (int i = max(0, total - S.nsd); i < total; ++i) wt.wait(full_d + i % S.nsd, fparity(i, S.nsd), true);
-    return;
   }
+  // adapters read later: into L2
+  if (a.shA[2] && tid < r * G2) prefetch_l2(a.shA[2] + tid * 64);
+  if (tid < nsp) {
+    if (a.shA[0]) prefetch_l2(a.shB[0] + static_cast<size_t>(sp0 + tid) * r);
+    if (a.shA[1]) prefetch_l2(a.shB[1] + static_cast<size_t>(sp0 + tid) * r);
+  }
+  if (a.shA[2] && tid >= 32 && tid < 32 + ndr) prefetch_l2(a.shB[2] + static_cast<size_t>(dr0 + tid - 32) * r);
+  if (a.rbias && tid >= 64 && tid < 64 + n8 && r0 + tid - 64 < a.E) prefetch_l2(a.rbias + r0 + tid - 64);
+  if (tid == 0) misc[0] = 0;
 
   // --------------------------------------------------------------------------- token images
   const uint8_t* img = a.smem_image ? sm + S.img : a.img;
   float* us = reinterpret_cast<float*>(sm + S.us);
   float* ic = reinterpret_cast<float*>(sm + S.ic);
   double* red = reinterpret_cast<double*>(sm + S.red);
-  if (a.shared_build) {
-    for (int t = cta; t < T; t += grid)
-      build_image(a, t, warp, kWarps, 0, red, a.img + static_cast<size_t>(t) * ldu, a.us + t * G, a.ic + t, true);
-    grid_arrive(a, B_IMAGE);
-    grid_wait(a, B_IMAGE, wt);
-    if (a.smem_image)
-      for (int i = tid; i < T * ldu / 16; i += kComp)
-        reinterpret_cast<uint4*>(sm + S.img)[i] = __ldcg(reinterpret_cast<const uint4*>(a.img) + i);
-    for (int i = tid; i < T * G; i += kComp) us[i] = __ldcg(a.us + i);
+  volatile int* failed = misc;
+  auto build = [&](int t, int wi, int warps, int team, uint8_t* row, float* u, float* c, bool write_u) {
+    if (a.x)
+      build_image<true>(a, t, wi, warps, team, red, row, u, c, write_u);
+    else
+      build_image<false>(a, t, wi, warps, team, red, row, u, c, write_u);
+  };
+  if (!a.smem_image) {
+    if (cta < T)
+      build(cta, warp, kWarps, 0, a.img + static_cast<size_t>(cta) * ldu, a.us + cta * G, a.ic + cta, true);
+    if (tid == 0) header_ready(a.bar, failed, a.err, a.timeout_ns);
+    grid_arrive(a.bar, B_IMAGE);
+    grid_wait(a.bar, B_IMAGE, false, failed, a.err, a.timeout_ns);
+#pragma unroll 1
+    for (int i = tid; i < T * G; i += kThreads) us[i] = __ldcg(a.us + i);
     if (tid < T) ic[tid] = __ldcg(a.ic + tid);
   } else {
-    int W = kWarps;
-    while (W > 1 && W * T > kWarps) W >>= 1;
-    const int teams = kWarps / W, team = warp / W;
-    for (int t = team; t < T; t += teams)
-      build_image(a, t, warp % W, W, team, red, sm + S.img + t * ldu, us + t * G, ic + t, t % grid == cta);
+    const int logW = T == 1 ? 4 : (T == 2 ? 3 : 2), W = 1 << logW, team = warp >> logW;  // at most 4 tokens
+    if (team < T)
+      build(team, warp & (W - 1), W, team, sm + S.img + team * ldu, us + team * G, ic + team, team == cta);
+    if (tid == 0) header_ready(a.bar, failed, a.err, a.timeout_ns);
   }
-  cta_sync();
+  named_sync(15, kThreads);
 
   // --------------------------------------------------------------------------- rows over all tokens: router, shared
   // gate (8 bits), the shared expert's gate and up LoRA A (fp16)
-  const int nA = (a.shA[0] ? r : 0) + (a.shA[1] ? r : 0);
-  {
-    const int nrows = a.E + 1 + nA, r0 = cta * nrows / grid, r1 = (cta + 1) * nrows / grid;
-    const int g0 = warp * G / kWarps, g1 = (warp + 1) * G / kWarps;
-    const int n8 = max(0, min(r1, a.E + 1) - r0);  // 8-bit rows r0 .. r0 + n8 - 1, then fp16 rows
-    const int R8 = qrow_bytes(a.H, 8);
-    for (int t0 = 0; t0 < T; t0 += 8) {
-      const uint8_t* col = img + static_cast<size_t>(min(t0 + g, T - 1)) * ldu;
-      const float* ua = us + min(t0 + 2 * tig, T - 1) * G;
-      const float* ub = us + min(t0 + 2 * tig + 1, T - 1) * G;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      if (n8 > 0) {
-        const int row = r0 + min(g, n8 - 1);
-        const uint8_t* rec = row < a.E ? a.router + static_cast<size_t>(row) * R8 : a.sgate;
-#pragma unroll 2
-        for (int gi = g0; gi < g1; ++gi) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(rec + gi * 64 + tig * 16));
-          const BFrag f = b_frag(col, gi, tig);
-          float ev[4] = {0.f, 0.f, 0.f, 0.f}, od[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint32_t m = 0x00FF00FFu;
-          mma16(ev, prmt(q.x, q.y, 0x4400) & m, 0, prmt(q.x, q.y, 0x6622) & m, 0, f.x.x, f.x.z);
-          mma16(od, prmt(q.x, q.y, 0x5511) & m, 0, prmt(q.x, q.y, 0x7733) & m, 0, f.x.y, f.x.w);
-          mma16(ev, prmt(q.z, q.w, 0x4400) & m, 0, prmt(q.z, q.w, 0x6622) & m, 0, f.y.x, f.y.z);
-          mma16(od, prmt(q.z, q.w, 0x5511) & m, 0, prmt(q.z, q.w, 0x7733) & m, 0, f.y.y, f.y.w);
-          const float s = half_at(rec + a.H + 2 * gi), b = half_at(rec + a.H + 2 * (G + gi));
-          acc[0] = fmaf(b, ua[gi], fmaf(s, fmaf(16.f, od[0], ev[0]), acc[0]));
-          acc[1] = fmaf(b, ub[gi], fmaf(s, fmaf(16.f, od[1], ev[1]), acc[1]));
-        }
-      }
-      if (g < n8) *reinterpret_cast<float2*>(scratch + (warp * 16 + g) * 8 + 2 * tig) = make_float2(acc[0], acc[1]);
-      const int nf = r1 - r0 - n8;
-      if (nf > 0) {
-        const int j = r0 + n8 + min(g, nf - 1) - (a.E + 1);  // LoRA row: gate's rows, then up's
-        const uint16_t* A = (a.shA[0] && j < r) ? a.shA[0] + static_cast<size_t>(j) * a.H
-                                                : a.shA[1] + static_cast<size_t>(a.shA[0] ? j - r : j) * a.H;
-        float ev[4] = {0.f, 0.f, 0.f, 0.f}, od[4] = {0.f, 0.f, 0.f, 0.f};
-        f16_rows<false>(A, A, g0, g1, col, ev, od);
-        if (g < nf)
-          *reinterpret_cast<float2*>(scratch + (warp * 16 + n8 + g) * 8 + 2 * tig) =
-              make_float2(fmaf(16.f, od[0], ev[0]), fmaf(16.f, od[1], ev[1]));
-      }
-      cta_sync();
-      for (int i = tid; i < (r1 - r0) * 8; i += kComp) {
-        const int row = i >> 3, t = t0 + (i & 7);
-        if (t < T) {
-          float v = 0.f;
-          for (int w = 0; w < kWarps; ++w) v += scratch[(w * 16 + row) * 8 + (i & 7)];
-          v *= ic[t];
-          const int j = r0 + row;
-          if (j < a.E)
-            a.logits[static_cast<size_t>(t) * a.E + j] = v * 0x1p24f + (a.rbias ? a.rbias[j] : 0.f);
-          else
-            a.aux[(j - a.E) * T + t] = j == a.E ? v * 0x1p24f : v;
-        }
-      }
-      cta_sync();
-    }
-  }
-  grid_arrive(a, B_LOGITS);
-
-  // --------------------------------------------------------------------------- shared expert's gate/up, raw
-  if (nst > 0) {
-    const int nb = (T + 15) / 16, units = nst * nb, W = units > 1 ? 8 : 16, teams = kWarps / W, team = warp / W;
-    float* part = scratch + team * (W * 16 * 16);
-    for (int un = 0; un < units; un += teams) {
-      const int q = un + team, ti = q / nb, t0 = (q % nb) * 16;
-      const bool on = q < units;
-      if (on) {
-        wt.wait(full_g + ti, 0);
-        gate_up_block<2>(a, img, us, ring + ti * S.stage_g, warp % W, W, part, [&](int c) { return min(t0 + c, T - 1); });
-      }
-      cta_sync();
-      if (on) {
-        for (int i = tid - team * W * 32; i < 8 * 16; i += W * 32) {
-          const int pr = i & 7, c = i >> 3, t = t0 + c;
-          if (8 * ti + pr < nsp && t < T) {
-            const float2 v = pair_sum<2>(part, W, pr, c);
-            sraw[t * 2 * nsp + 2 * (8 * ti + pr)] = v.x * ic[t];
-            sraw[t * 2 * nsp + 2 * (8 * ti + pr) + 1] = v.y * ic[t];
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const int first = kind ? r0 + n8 : r0, n = kind ? r1 - first : n8;
+    if (n <= 0) continue;
+    const int row = first + min(g, n - 1);
+#pragma unroll 1
+    for (int b = 0; b < nblk; ++b) {
+      const uint8_t* col = img + static_cast<size_t>(min(8 * b + g, T - 1)) * ldu;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kind == 0) {
+        const float* ua = us + min(8 * b + 2 * tig, T - 1) * G;
+        const float* ub = us + min(8 * b + 2 * tig + 1, T - 1) * G;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int gi = g0 + i;
+          if (gi < g1) {
+            const uint4* p = reinterpret_cast<const uint4*>(col + gi * 128 + tig * 32);
+            const uint4 x = p[0], y = p[1], q = q8[i];
+            float ev[4] = {0.f, 0.f, 0.f, 0.f}, od[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t m = 0x00FF00FFu;
+            mma16(ev, prmt(q.x, q.y, 0x4400) & m, 0, prmt(q.x, q.y, 0x6622) & m, 0, x.x, x.z);
+            mma16(od, prmt(q.x, q.y, 0x5511) & m, 0, prmt(q.x, q.y, 0x7733) & m, 0, x.y, x.w);
+            mma16(ev, prmt(q.z, q.w, 0x4400) & m, 0, prmt(q.z, q.w, 0x6622) & m, 0, y.x, y.z);
+            mma16(od, prmt(q.z, q.w, 0x5511) & m, 0, prmt(q.z, q.w, 0x7733) & m, 0, y.y, y.w);
+            const float s = lo_half(sb8[i]), o = hi_half(sb8[i]);
+            v[0] = fmaf(o, ua[gi], fmaf(s, fmaf(16.f, od[0], ev[0]), v[0]));
+            v[1] = fmaf(o, ub[gi], fmaf(s, fmaf(16.f, od[1], ev[1]), v[1]));
           }
         }
+      } else {
+        const int j = row - (a.E + 1);  // gate's rows, then up's
+        const uint16_t* A = (a.shA[0] && j < r) ? a.shA[0] + static_cast<size_t>(j) * a.H
+                                                : a.shA[1] + static_cast<size_t>(a.shA[0] ? j - r : j) * a.H;
+        f16_rows(A, A, g0, g1, col, v);
       }
-      cta_sync();
+      if (g < n) *reinterpret_cast<float2*>(scratch + ((warp * 4 + b) * 8 + g) * 8 + 2 * tig) = make_float2(v[0], v[1]);
     }
-    if (tid == 0)
-      for (int i = 0; i < nst; ++i) bar_arrive(empty_g + i);
+    named_sync(15, kThreads);
+    {  // one thread per (row, token): up to 8 rows x 32 tokens
+      const int q = tid >> 5, t = tid & 31;
+      if (q < n && t < T) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < kWarps; ++w) v += scratch[((w * 4 + (t >> 3)) * 8 + q) * 8 + (t & 7)];
+        v *= ic[t];
+        const int j = first + q;
+        if (j < a.E)
+          a.logits[static_cast<size_t>(t) * a.E + j] = v * 0x1p24f + (a.rbias ? __ldg(a.rbias + j) : 0.f);
+        else if (j == a.E)
+          a.aux[t * (4 + 2 * r)] = v * 0x1p24f;
+        else
+          a.aux[t * (4 + 2 * r) + 4 + j - (a.E + 1)] = v;
+      }
+    }
+    named_sync(15, kThreads);
+  }
+  grid_arrive(a.bar, B_LOGITS);
+
+  // --------------------------------------------------------------------------- shared expert's gate/up, raw
+#pragma unroll 1
+  for (int ti = 0; ti < nst; ++ti) {
+#pragma unroll 1
+    for (int task = warp; task < U * sh_ways; task += kWarps) {
+      const int u = task & (U - 1);
+      if (ti > 0) {
+        const uint8_t* src = a.shared + static_cast<size_t>(2 * (sp0 + 8 * ti)) * RGU;
+        const int n = min(8, nsp - 8 * ti);
+        issue_unit(ring32, plan, src + 128 * u, src + 8 * u, n, n);
+        cp_commit();
+      }
+      cp_wait<0>();
+#pragma unroll 1
+      for (int b = task >> a.logU; b < nblk; b += sh_ways) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        gate_up_unit(ring, img + static_cast<size_t>(min(8 * b + g, T - 1)) * ldu + u * 512,
+                     us + min(8 * b + 2 * tig, T - 1) * G + 4 * u, us + min(8 * b + 2 * tig + 1, T - 1) * G + 4 * u, acc);
+        *reinterpret_cast<float4*>(scratch + ((b * U + u) * 32 + lane) * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      }
+      __syncwarp();
+    }
+    named_sync(15, kThreads);
+    if (warp < nblk) {  // block `warp`: (pair g, tokens 2 tig and 2 tig + 1)
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int u = 0; u < U; ++u) {
+        const float4 p = *reinterpret_cast<const float4*>(scratch + ((warp * U + u) * 32 + lane) * 4);
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+      }
+      const int t = 8 * warp + 2 * tig, pr = 8 * ti + g;
+      if (pr < nsp) {
+        float2* o = reinterpret_cast<float2*>(sraw) + pr;
+        if (t < T) o[t * 16] = make_float2(v.x * 0x1p24f * ic[t], v.z * 0x1p24f * ic[t]);
+        if (t + 1 < T) o[(t + 1) * 16] = make_float2(v.y * 0x1p24f * ic[t + 1], v.w * 0x1p24f * ic[t + 1]);
+      }
+    }
+    named_sync(15, kThreads);
   }
 
   // --------------------------------------------------------------------------- top-K, gating, the expert list
-  grid_wait(a, B_LOGITS, wt);
   uint32_t* mask = reinterpret_cast<uint32_t*>(scratch);  // [256 experts][8 words]: the slots that chose an expert
-  for (int i = tid; i < kMaxE * 8; i += kComp) mask[i] = 0;
-  cta_sync();
-  for (int t = warp; t < T; t += kWarps) {
-    const float* lg = a.logits + static_cast<size_t>(t) * a.E;
-    uint32_t key[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = lane + 32 * i;
-      uint32_t k = 0;
-      if (e < a.E) {
-        const float v = __ldcg(lg + e);
-        const uint32_t b = __float_as_uint(v);
-        k = v != v ? 1u : b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);  // order of the floats; NaN last
-      }
-      key[i] = k;
-    }
-    int my_e = 0;
-    float my_l = -INFINITY;
-    for (int k = 0; k < K; ++k) {
-      uint32_t best = key[0];
-      int bi = 0;
-#pragma unroll
-      for (int i = 1; i < 8; ++i)
-        if (key[i] > best) best = key[i], bi = i;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      const int e = static_cast<int>(
-          __reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffu));
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e == lane + 32 * i) key[i] = 0;
-      if (lane == k) my_e = min(e, a.E - 1);
-    }
-    if (lane < K && cta == 0) a.idx[t * K + lane] = my_e;
-    if (a.exec_idx && lane < K) my_e = min(max(a.exec_idx[t * K + lane], 0), a.E - 1);
-    if (lane < K) my_l = __ldcg(lg + my_e);
-    float mx = my_l;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ex = lane < K ? expf(my_l - mx) : 0.f;
-    float den = ex;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (lane < K) {
-      const int s = t * K + lane;
-      sel[s] = my_e;
-      sw[s] = ex / den;
-      atomicOr(mask + my_e * 8 + (s >> 5), 1u << (s & 31));
-      if (cta == 0) a.w[s] = ex / den;
-    }
-  }
+  for (int i = tid; i < kMaxE * 2; i += kThreads) reinterpret_cast<uint4*>(mask)[i] = make_uint4(0, 0, 0, 0);
+  grid_wait(a.bar, B_LOGITS, false, failed, a.err, a.timeout_ns);
+#pragma unroll 1
+  for (int t = warp; t < T; t += kWarps) route_token(a, t, sel, sw, mask);
   float* gate = reinterpret_cast<float*>(sm + S.gate);
-  if (tid < T) gate[tid] = sigmoid(__ldcg(a.aux + tid));
-  cta_sync();
+  if (tid < T) gate[tid] = sigmoid(__ldcg(a.aux + tid * (4 + 2 * r)));
+  named_sync(15, kThreads);
   if (warp < 8) {  // chosen experts in ascending order, their slots in ascending order, the down elements
     int cnt = 0;
 #pragma unroll
@@ -728,14 +826,21 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     if (lane == 31) tot[2 * warp] = v, tot[2 * warp + 1] = __popc(bal);
     named_sync(1, 256);
     int off = v - own, d = __popc(bal & ((1u << lane) - 1));
+#pragma unroll 1
     for (int w = 0; w < warp; ++w) off += tot[2 * w], d += tot[2 * w + 1];
     int so = off & 0xffff, eo = sh_blocks + (off >> 16);
     if (cnt > 0) {
       dist[d] = tid;
       start[d] = so;
+#pragma unroll 1
       for (int b = 0; b < cnt; b += kSlotBlock) els[eo++] = d | (so + b) << 9 | min(kSlotBlock, cnt - b) << 20;
+#pragma unroll 1
       for (int i = 0; i < 8; ++i)
-        for (uint32_t m = mask[tid * 8 + i]; m; m &= m - 1) slots[so++] = 32 * i + __ffs(m) - 1;
+#pragma unroll 1
+        for (uint32_t m = mask[tid * 8 + i]; m; m &= m - 1) {
+          const int s = 32 * i + __ffs(m) - 1;
+          slots[so++] = s | static_cast<int>(s * a.kmul >> 16) << 16;
+        }
     }
     if (tid == 255) {
       const int D = d + (cnt > 0);
@@ -745,19 +850,22 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     }
     if (tid < sh_blocks) els[tid] = 511 | (tid * kSlotBlock) << 9 | min(kSlotBlock, T - tid * kSlotBlock) << 20;
   }
-  all_sync();
+  named_sync(15, kThreads);
   const int D = misc[1], nel = misc[2];
 
   // --------------------------------------------------------------------------- routed gate/up adapters: A u
   if (a.exAgu) {
     const int rows = 2 * r, total = D * rows;
+#pragma unroll 1
     for (int q = cta * kWarps + warp; q < total; q += grid * kWarps) {
       const int d = q / rows, i = q - d * rows, e = dist[d];
       const uint16_t* A = a.exAgu + (static_cast<size_t>(e) * rows + i) * a.H;
+#pragma unroll 1
       for (int s = start[d]; s < start[d + 1]; ++s) {
-        const int t = slots[s] / K;
+        const int sl = slots[s] & 0xffff, t = slots[s] >> 16;
         const uint8_t* row = img + static_cast<size_t>(t) * ldu;
         float v = 0.f;
+#pragma unroll 1
         for (int b = lane; b < a.H / 8; b += 32) {
           const uint4 p = __ldg(reinterpret_cast<const uint4*>(A) + b), x = *reinterpret_cast<const uint4*>(row + 16 * b);
           v = dot2_mix(prmt(p.x, p.z, 0x5410), x.x, v);
@@ -767,212 +875,292 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
           v = fmaf(16.f, o, v);
         }
         v = warp_reduce(v);
-        if (lane == 0) a.tgu[(static_cast<size_t>(slots[s]) * 2 + i / r) * r + i % r] = v * ic[t];
+        if (lane == 0) a.tgu[static_cast<size_t>(sl) * 2 * r + i] = v * ic[t];
       }
     }
-    grid_arrive(a, B_EXGU);
-    grid_wait(a, B_EXGU, wt);
-  }
-
-  // --------------------------------------------------------------------------- shared expert's hidden values
-  for (int i = tid; i < T * nsp; i += kComp) {
-    const int t = i / nsp, j = sp0 + i - t * nsp;
-    float x = sraw[2 * i], y = sraw[2 * i + 1];
-    const float* ta = a.aux + T + t;
-    if (a.shA[0]) {
-      float v = 0.f;
-      for (int k = 0; k < r; ++k) v = fmaf(half_bits_to_float(a.shB[0][static_cast<size_t>(j) * r + k]), __ldcg(ta + k * T), v);
-      x = fmaf(a.lora_scale, v, x);
-      ta += r * T;
-    }
-    if (a.shA[1]) {
-      float v = 0.f;
-      for (int k = 0; k < r; ++k) v = fmaf(half_bits_to_float(a.shB[1][static_cast<size_t>(j) * r + k]), __ldcg(ta + k * T), v);
-      y = fmaf(a.lora_scale, v, y);
-    }
-    store_h(a, TK + t, j, x, y);
+    grid_arrive(a.bar, B_EXGU);
+    grid_wait(a.bar, B_EXGU, false, failed, a.err, a.timeout_ns);
   }
 
   // --------------------------------------------------------------------------- chosen experts' gate/up
+  // The tiles (8 pairs) of all chosen experts, one after the other, are split evenly over the CTAs and there over teams
+  // of W warps; the W warps of a team split the units.  A warp's time goes by tiles x units; a team of more than one
+  // joins its sums at each tile, charged as one unit.
   {
-    const int lo = static_cast<int>(static_cast<long long>(cta) * (D << a.logI) / grid);
-    const int hi = static_cast<int>(static_cast<long long>(cta + 1) * (D << a.logI) / grid);
-    int nt = 0;
-    for (int pos = lo; pos < hi; ++nt) pos += next_tile(pos, hi, a.logI).n;
-    int W = nt >= 8 ? 4 : (nt >= 2 ? 8 : 16);
-    const int teams = kWarps / W, team = warp / W, wi = warp % W, ltid = tid - team * W * 32;
-    float* part = scratch + team * (W * 16 * 16);
-    int n = nst, q = 0;
-    for (int pos = lo; pos < hi; ++n, ++q) {
-      const Tile tl = next_tile(pos, hi, a.logI);
-      pos += tl.n;
-      if (q % teams != team) continue;
-      const int s = n % S.nsg, e = dist[tl.d], s0 = start[tl.d], cnt = start[tl.d + 1] - s0;
-      const uint8_t* stage = ring + s * S.stage_g;
-      ring_wait(wt, turn_g, full_g, n, S.nsg);
-      for (int b = 0; b < cnt;) {
-        const bool one = cnt - b <= 8;
-        auto token = [&](int c) { return slots[s0 + min(b + c, cnt - 1)] / K; };
-        if (one)
-          gate_up_block<1>(a, img, us, stage, wi, W, part, token);
-        else
-          gate_up_block<2>(a, img, us, stage, wi, W, part, token);
-        team_sync(team, W);
-        const int cols = one ? 8 : 16;
-        for (int i = ltid; i < 8 * cols; i += 32 * W) {
-          const int pr = i & 7, c = i >> 3;
-          if (pr < tl.n && b + c < cnt) {
-            const int slot = slots[s0 + b + c], j = tl.p0 + pr;
-            float2 v = one ? pair_sum<1>(part, W, pr, c) : pair_sum<2>(part, W, pr, c);
-            const float f = ic[slot / K];
-            v.x *= f;
-            v.y *= f;
-            if (a.exAgu) {
-              const uint16_t* B = a.exBgu + (static_cast<size_t>(e) * 2 * a.I + 2 * j) * r;
-              const float* t = a.tgu + static_cast<size_t>(slot) * 2 * r;
-              v.x = fmaf(a.lora_scale, dot_r(B, t, r), v.x);
-              v.y = fmaf(a.lora_scale, dot_r(B + r, t + r, r), v.y);
-            }
-            store_h(a, slot, j, v.x, v.y);
+    const int logt = a.logI - 3, nt = D << logt, c0 = share(cta, nt, a.gmul), cn = share(cta + 1, nt, a.gmul) - c0;
+    int logW = 0, best = 1 << 30;
+#pragma unroll 1
+    for (int lw = 0; lw <= 3 && lw <= a.logU; ++lw) {
+      const int ts = kWarps >> lw, cost = ((cn + ts - 1) / ts) * ((U >> lw) + (lw > 0));
+      if (cost < best) best = cost, logW = lw;
+    }
+    const int W = 1 << logW, wi = warp & (W - 1), team = warp >> logW, ts = kWarps >> logW;
+    const int lo = c0 + team * cn / ts, hi = c0 + (team + 1) * cn / ts;
+    const int u0 = wi * (U >> logW), u1 = u0 + (U >> logW);
+    const int tmask = (1 << logt) - 1;
+    // the item being copied: base of its tile's records, and what follows it
+    int ipos = lo, ib = 0, iu = u0;
+    const uint8_t* ibase = nullptr;
+    auto open = [&]() {
+      ibase = a.pool + dist[ipos >> logt] * a.stride + static_cast<size_t>(16 * (ipos & tmask)) * RGU;
+    };
+    if (lo < hi) open();
+    uint32_t wr = ring32;
+    const uint32_t ring_end = ring32 + kBuf * kUnitBytes;
+    auto copy_next = [&]() {
+      if (ipos < hi) {
+        issue_unit(wr, plan, ibase + 128 * iu, ibase + 8 * iu, 8, 8);
+        if (++iu == u1) {
+          iu = u0;
+          ib += 8;
+          const int d = ipos >> logt;
+          if (ib >= start[d + 1] - start[d]) {
+            ib = 0;
+            if (++ipos < hi) open();
           }
         }
-        b += cols;
-        team_sync(team, W);
       }
-      if (ltid == 0) bar_arrive(empty_g + s);
-    }
-  }
-  grid_arrive(a, B_HIDDEN);
-  grid_wait(a, B_HIDDEN, wt);
+      cp_commit();
+      if ((wr += kUnitBytes) == ring_end) wr = ring32;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kBuf - 1; ++i) copy_next();
 
-  // --------------------------------------------------------------------------- LoRA A on the hidden values
-  const uint8_t* hb = reinterpret_cast<const uint8_t*>(a.h);
-  const size_t hrow = static_cast<size_t>(a.I) * 2;  // bytes of one hi or lo row
-  auto lora_h = [&](const uint16_t* A, int m0, int pos_of_col, float (&v)[2]) {  // rows m0 + g, m0 + g + 8
-    const uint16_t* ra = A + static_cast<size_t>(min(m0 + g, r - 1)) * a.I;
-    const uint16_t* rb = A + static_cast<size_t>(min(m0 + g + 8, r - 1)) * a.I;
-    float ev[4] = {0.f, 0.f, 0.f, 0.f}, od[4] = {0.f, 0.f, 0.f, 0.f};
-    f16_rows<true>(ra, rb, 0, G2, hb + (static_cast<size_t>(pos_of_col) * 2 + (g & 1)) * hrow, ev, od);
-    v[0] = fmaf(fmaf(16.f, od[1], ev[1]), 0x1p-11f, fmaf(16.f, od[0], ev[0]));
-    v[1] = fmaf(fmaf(16.f, od[3], ev[3]), 0x1p-11f, fmaf(16.f, od[2], ev[2]));
-  };
-  const int mts = (r + 15) / 16;
-  if (a.exA) {  // each (block of slots, 16 rows of A) once in the grid
-    for (int q = cta + grid * warp; q < (nel - sh_blocks) * mts; q += grid * kWarps) {
-      const int el = els[sh_blocks + q / mts], m0 = (q % mts) * 16, d = el & 511, s0 = (el >> 9) & 511, n = el >> 20;
-      float v[2];
-      lora_h(a.exA + static_cast<size_t>(dist[d]) * r * a.I, m0, slots[s0 + min(g >> 1, n - 1)], v);
-      if (tig < n) {
-        float* t = a.tex + static_cast<size_t>(slots[s0 + tig]) * r;
-        if (m0 + g < r) t[m0 + g] = v[0];
-        if (m0 + g + 8 < r) t[m0 + g + 8] = v[1];
-      }
+    // the shared expert's hidden values while the first copies are under way: a pair of lanes per (token, pair)
+#pragma unroll 1
+    for (int t = warp; t < T && nsp > 0; t += kWarps) {
+      const int pr = min(lane >> 1, nsp - 1), up = lane & 1;
+      const float2 v = reinterpret_cast<const float2*>(sraw)[t * 16 + pr];
+      float x = up ? v.y : v.x;
+      const uint16_t* B = up ? a.shB[1] : a.shB[0];
+      if (up ? a.shA[1] != nullptr : a.shA[0] != nullptr)
+        x = fmaf(a.lora_scale, dot_r(B + static_cast<size_t>(sp0 + pr) * r, a.aux + t * (4 + 2 * r) + 4 + (up && a.shA[0] ? r : 0), r), x);
+      __syncwarp();
+      const float y = __shfl_xor_sync(0xffffffffu, x, 1);
+      if (!up && lane < 2 * nsp) store_h(a, TK + t, sp0 + pr, x, y);
     }
-    grid_arrive(a, B_EXDOWN);
-  }
-  float* td = reinterpret_cast<float*>(sm + S.td);
-  if (a.shA[2]) {
-    for (int q = kWarps - 1 - warp; q < sh_blocks * mts; q += kWarps) {
-      const int t0 = (q / mts) * kSlotBlock, m0 = (q % mts) * 16;
-      float v[2];
-      lora_h(a.shA[2], m0, TK + min(t0 + (g >> 1), T - 1), v);
-      if (t0 + tig < T) {
-        if (m0 + g < r) td[(t0 + tig) * kMaxR + m0 + g] = v[0];
-        if (m0 + g + 8 < r) td[(t0 + tig) * kMaxR + m0 + g + 8] = v[1];
+
+    uint8_t* rd = ring;
+    int pos = lo, b = 0, u = u0, flip = 0;
+    int d = 0, s0 = 0, cnt = 0;
+    const uint8_t* col = nullptr;
+    const float *ua = nullptr, *ub = nullptr;
+    auto columns = [&]() {  // of item (pos, b)
+      d = pos >> logt;
+      s0 = start[d];
+      cnt = start[d + 1] - s0;
+      const int c0 = s0 + b, cl = s0 + cnt - 1;
+      col = img + static_cast<size_t>(slots[min(c0 + g, cl)] >> 16) * ldu;
+      ua = us + (slots[min(c0 + 2 * tig, cl)] >> 16) * G;
+      ub = us + (slots[min(c0 + 2 * tig + 1, cl)] >> 16) * G;
+    };
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (lo < hi) columns();
+#pragma unroll 1
+    while (pos < hi) {
+      copy_next();
+      cp_wait<kBuf - 1>();
+      gate_up_unit(rd, col + u * 512, ua + 4 * u, ub + 4 * u, acc);
+      if ((rd += kUnitBytes) == ring + kBuf * kUnitBytes) rd = ring;
+      if (++u == u1) {
+        u = u0;
+        bool mine = true;
+        if (W > 1) {  // the team's first warp adds up; the two buffers take turns, so one barrier a tile does
+          float4* p = reinterpret_cast<float4*>(scratch) + flip * (kWarps * 32);
+          p[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          flip ^= 1;
+          team_sync(team, W);
+          mine = wi == 0;
+          if (mine) {
+#pragma unroll 1
+            for (int w = 1; w < W; ++w) {
+              const float4 v = p[(warp + w) * 32 + lane];
+              acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+            }
+          }
+        }
+        if (mine) {
+          const int j = (pos & tmask) * 8 + g;
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            const int q = 2 * tig + c;
+            if (b + q >= cnt) break;
+            const int sl = slots[s0 + b + q] & 0xffff;
+            const float k = ic[slots[s0 + b + q] >> 16] * 0x1p24f;
+            float x = (c ? acc[1] : acc[0]) * k, y = (c ? acc[3] : acc[2]) * k;
+            if (a.exAgu) {
+              const uint16_t* B = a.exBgu + (static_cast<size_t>(dist[d]) * 2 * a.I + 2 * j) * r;
+              const float* t = a.tgu + static_cast<size_t>(sl) * 2 * r;
+              x = fmaf(a.lora_scale, dot_r(B, t, r), x);
+              y = fmaf(a.lora_scale, dot_r(B + r, t + r, r), y);
+            }
+            store_h(a, sl, j, x, y);
+          }
+        }
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        b += 8;
+        if (b >= cnt) b = 0, ++pos;
+        if (pos < hi) columns();
       }
+      __syncwarp();
     }
   }
+  grid_arrive(a.bar, B_HIDDEN);
 
   // --------------------------------------------------------------------------- down projections
-  const int NS = TK + T, RS = nrt * kTileRows;  // y [W][slot][RS]
-  int Wd = 1;
-  while (Wd < 8 && nrt * nel * Wd * 2 <= kWarps && G2 >= 2 * Wd) Wd *= 2;
-  {
-    const int teams = kWarps / Wd, team = warp / Wd, wi = warp % Wd;
-    const int g0 = wi * G2 / Wd, g1 = (wi + 1) * G2 / Wd;
-    for (int i = team; i < nrt * nel; i += teams) {
-      const int rt = i / nel, el = els[i - rt * nel], d = el & 511, s0 = (el >> 9) & 511, n = el >> 20, s = i % S.nsd;
-      const int cs = min(g >> 1, n - 1);
-      const int pos = d == 511 ? TK + s0 + cs : slots[s0 + cs];
-      const uint8_t* col = hb + (static_cast<size_t>(pos) * 2 + (g & 1)) * hrow;
-      const uint8_t* ra = ring + s * S.stage_d + g * S.sd;
-      const uint8_t* rb = ra + 8 * S.sd;
-      const bool ones = g == 7;  // row 15
-      if (ones) rb = ra;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      ring_wait(wt, turn_d, full_d, i, S.nsd);
-#pragma unroll 4
-      for (int gi = g0; gi < g1; ++gi) {
-        const BFrag f = b_frag_l2(col, gi, tig);
-        const uint2 wa = *reinterpret_cast<const uint2*>(ra + gi * 32 + tig * 8);
-        const uint2 wb = *reinterpret_cast<const uint2*>(rb + gi * 32 + tig * 8);
-        const float sc0 = half_at(ra + a.I / 2 + 2 * gi), b0 = half_at(ra + a.I / 2 + 2 * (G2 + gi));
-        const float sc1 = half_at(rb + a.I / 2 + 2 * gi), b1 = half_at(rb + a.I / 2 + 2 * (G2 + gi));
-        // codes times 2^-22 (and 16 of that).  The MMA aligns its products by their exponents, and a subnormal counts
-        // with the smallest one, so two more of the mantissa's bits in use keep two more of h's 11 in the sum
-        // (u's 8 fit either way): 3e-6 of the result against 7e-7.
-        const uint32_t lo = 0x003C003Cu, hi = 0x03C003C0u;
-        const uint32_t p0 = wa.x << 2, p1 = wa.x >> 6, p2 = wa.y << 2, p3 = wa.y >> 6;
-        const uint32_t q0 = wb.x << 2, q1 = wb.x >> 6, q2 = wb.y << 2, q3 = wb.y >> 6;
-        const uint32_t one = 0x3C003C00u, sixteen = 0x4C004C00u;  // row 15: the plain sum (odd entries are / 16)
-        float dd[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16(dd, p0 & lo, ones ? one : q0 & lo, p0 & hi, ones ? sixteen : q0 & hi, f.x.x, f.x.y);
-        mma16(dd, p1 & lo, ones ? one : q1 & lo, p1 & hi, ones ? sixteen : q1 & hi, f.x.z, f.x.w);
-        mma16(dd, p2 & lo, ones ? one : q2 & lo, p2 & hi, ones ? sixteen : q2 & hi, f.y.x, f.y.y);
-        mma16(dd, p3 & lo, ones ? one : q3 & lo, p3 & hi, ones ? sixteen : q3 & hi, f.y.z, f.y.w);
-        const float u0 = __shfl_sync(0xffffffffu, dd[2], 28 + tig) * 0x1p-22f;
-        const float u1 = __shfl_sync(0xffffffffu, dd[3], 28 + tig) * 0x1p-22f;
-        acc[0] = fmaf(b0, u0, fmaf(sc0, dd[0], acc[0]));
-        acc[1] = fmaf(b0, u1, fmaf(sc0, dd[1], acc[1]));
-        acc[2] = fmaf(b1, u0, fmaf(sc1, dd[2], acc[2]));
-        acc[3] = fmaf(b1, u1, fmaf(sc1, dd[3], acc[3]));
+  // Elements: (row tile, a block of up to 4 slots of one expert), dealt out to teams of Wd warps that split the units.
+  const int NS = TK + T, RS = nrt * 16, total = nrt * nel;  // y [Wd][slot][RS]
+  int logWd = 0;
+  while (logWd < 3 && total << (logWd + 1) <= kWarps && U2 >> (logWd + 1) > 0) ++logWd;
+  const int Wd = 1 << logWd, teams = kWarps >> logWd, wi = warp & (Wd - 1);
+  const int u0 = wi * (U2 >> logWd), u1 = u0 + (U2 >> logWd);
+  plan.make(RDN, G2, 1, 8);
+  int ie = warp >> logWd, iu = u0;  // next to copy
+  uint32_t wr = ring32;
+  uint8_t* rd = ring;
+  const uint8_t* ibase = nullptr;
+  int in = 0;
+  auto open = [&]() {
+    const int rt = ie < nel ? 0 : 1, d = els[ie - rt * nel] & 511;
+    in = min(rt_rows, ndr - rt * rt_rows);
+    ibase = (d == 511 ? a.shared : a.pool + dist[d] * a.stride) + dn_off + static_cast<size_t>(dr0 + rt * rt_rows) * RDN;
+  };
+  if (ie < total) open();
+  auto copy_next = [&]() {
+    if (ie < total) {
+      issue_unit(wr, plan, ibase + 128 * iu, ibase + 8 * iu, min(8, in), in - 8);
+      if (++iu == u1) {
+        iu = u0;
+        ie += teams;
+        if (ie < total) open();
       }
+    }
+    cp_commit();
+    if ((wr += kUnitBytes) == ring32 + kBuf * kUnitBytes) wr = ring32;
+  };
+  cp_wait<0>();
+#pragma unroll 1
+  for (int i = 0; i < kBuf - 1; ++i) copy_next();
+  grid_wait(a.bar, B_HIDDEN, !a.exA, failed, a.err, a.timeout_ns);
+
+  const uint8_t* hb = reinterpret_cast<const uint8_t*>(a.h);
+  const size_t hrow = static_cast<size_t>(a.I) * 2;  // bytes of one hi or lo row
+  const int logm = r > 16 ? 1 : 0;  // 16-row tiles of A: 1 or 2
+  float* td = reinterpret_cast<float*>(sm + S.td);
+  // LoRA A on hidden values: routed, each (block of slots, 16 rows of A) once in the grid; shared, in every CTA, with
+  // the groups split over as many warps as there are (partial sums [part][token][kMaxR])
+  int logp = 0;
+  while (logp < 3 && (sh_blocks << logm) << (logp + 1) <= kWarps && G2 >> (logp + 1) > 0) ++logp;
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const uint16_t* A = kind ? a.shA[2] : a.exA;
+    if (!A) continue;
+    const int tasks = (kind ? sh_blocks << logp : nel - sh_blocks) << logm;
+#pragma unroll 1
+    for (int q = kind ? kWarps - 1 - warp : cta + grid * warp; q < tasks; q += kind ? kWarps : grid * kWarps) {
+      const int m0 = (q & ((1 << logm) - 1)) * 16, part = kind ? (q >> logm) & ((1 << logp) - 1) : 0;
+      const int ei = kind ? q >> (logm + logp) : q >> logm, el = els[(kind ? 0 : sh_blocks) + ei];
+      const int d = el & 511, s0 = (el >> 9) & 511, n = el >> 20, cs = s0 + min(g >> 1, n - 1);
+      const uint16_t* M = A + (kind ? 0 : static_cast<size_t>(dist[d]) * r * a.I);
+      const int pos = kind ? TK + cs : slots[cs] & 0xffff, span = kind ? G2 >> logp : G2;
+      float v[4];
+      f16_rows(M + static_cast<size_t>(min(m0 + g, r - 1)) * a.I, M + static_cast<size_t>(min(m0 + g + 8, r - 1)) * a.I,
+                     part * span, (part + 1) * span, hb + (static_cast<size_t>(pos) * 2 + (g & 1)) * hrow, v);
       if (tig < n) {
-        const int p = d == 511 ? TK + s0 + tig : slots[s0 + tig];
-        float* y = scratch + (wi * NS + p) * RS + rt * kTileRows;
-        y[g] = fmaf(acc[1], 0x1p-11f, acc[0]) * 0x1p22f;
-        if (!ones) y[g + 8] = fmaf(acc[3], 0x1p-11f, acc[2]) * 0x1p22f;
+        float* o = kind ? td + (part * T + s0 + tig) * kMaxR : a.tex + static_cast<size_t>(slots[s0 + tig] & 0xffff) * r;
+        if (m0 + g < r) o[m0 + g] = fmaf(v[1], 0x1p-11f, v[0]);
+        if (m0 + g + 8 < r) o[m0 + g + 8] = fmaf(v[3], 0x1p-11f, v[2]);
       }
-      team_sync(team, Wd);
-      if (wi == 0 && lane == 0) bar_arrive(empty_d + s);
+    }
+    if (kind == 0) grid_arrive(a.bar, B_EXDOWN);
+  }
+
+  {
+    int i = warp >> logWd, el = 0;
+    const uint8_t* col = nullptr;
+    auto column = [&]() {
+      el = els[i < nel ? i : i - nel];
+      const int cs = ((el >> 9) & 511) + min(g >> 1, (el >> 20) - 1);
+      col = hb + (static_cast<size_t>((el & 511) == 511 ? TK + cs : slots[cs] & 0xffff) * 2 + (g & 1)) * hrow;
+    };
+    if (i < total) column();
+    int u = u0;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    while (i < total) {
+      copy_next();
+      cp_wait<kBuf - 1>();
+      down_unit(rd, col + u * 512, G2 >= 4, acc);
+      if ((rd += kUnitBytes) == ring + kBuf * kUnitBytes) rd = ring;
+      if (++u == u1) {
+        u = u0;
+        const int s0 = (el >> 9) & 511;
+        if (tig < el >> 20) {
+          const int p = (el & 511) == 511 ? TK + s0 + tig : slots[s0 + tig] & 0xffff;
+          float* y = scratch + (wi * NS + p) * RS + (i < nel ? 0 : 16);
+          y[g] = fmaf(acc[1], 0x1p-11f, acc[0]) * 0x1p22f;
+          if (g < 7) y[g + 8] = fmaf(acc[3], 0x1p-11f, acc[2]) * 0x1p22f;
+        }
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        i += teams;
+        if (i < total) column();
+      }
+      __syncwarp();
     }
   }
   if (a.exA)
-    grid_wait(a, B_EXDOWN, wt);
+    grid_wait(a.bar, B_EXDOWN, true, failed, a.err, a.timeout_ns);
   else
-    cta_sync();
+    named_sync(15, kThreads);
 
   // --------------------------------------------------------------------------- combine
-  for (int i = tid; i < T * ndr; i += kComp) {
-    const int t = i / ndr, row = i - t * ndr, rt = row / rt_rows, o = rt * kTileRows + row - rt * rt_rows;
+  const int t = tid >> 4;  // a thread per (token, row of a tile)
+#pragma unroll 1
+  for (int rt = 0; rt < nrt && t < T; ++rt) {
+    const int row = rt * rt_rows + (tid & 15), o = rt * 16 + (tid & 15);
+    if ((tid & 15) >= rt_rows || row >= ndr) continue;
     const int hr = dr0 + row;
-    auto y_of = [&](int pos) {
-      float v = 0.f;
-      for (int w = 0; w < Wd; ++w) v += scratch[(w * NS + pos) * RS + o];
-      return v;
-    };
-    float v = 0.f;
-    for (int k = 0; k < K; ++k) {
-      const int s = t * K + k;
-      float y = y_of(s);
-      if (a.exA)
-        y = fmaf(a.lora_scale, dot_r(a.exB + (static_cast<size_t>(sel[s]) * a.H + hr) * r, a.tex + static_cast<size_t>(s) * r, r), y);
-      v = fmaf(sw[s], y, v);
+    float out = 0.f;
+#pragma unroll 1
+    for (int k = 0; k <= K; ++k) {  // the K experts in order, then the shared one
+      const int s = k < K ? t * K + k : TK + t;
+      float y = 0.f;
+#pragma unroll 1
+      for (int w = 0; w < Wd; ++w) y += scratch[(w * NS + s) * RS + o];
+      if (k < K) {
+        if (a.exA)
+          y = fmaf(a.lora_scale, dot_r(a.exB + (static_cast<size_t>(sel[s]) * a.H + hr) * r, a.tex + static_cast<size_t>(s) * r, r), y);
+        out = fmaf(sw[s], y, out);
+      } else {
+        if (a.shA[2]) {
+          float l = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < r; i += 8) {
+            const uint4 b = __ldg(reinterpret_cast<const uint4*>(a.shB[2] + static_cast<size_t>(hr) * r + i));
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int w = 0; w < 1 << logp; ++w) {
+              const float4* p = reinterpret_cast<const float4*>(td + (w * T + t) * kMaxR + i);
+              const float4 x = p[0], z = p[1];
+              v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += z.x, v[5] += z.y, v[6] += z.z, v[7] += z.w;
+            }
+            l = fmaf(lo_half(b.x), v[0], l), l = fmaf(hi_half(b.x), v[1], l);
+            l = fmaf(lo_half(b.y), v[2], l), l = fmaf(hi_half(b.y), v[3], l);
+            l = fmaf(lo_half(b.z), v[4], l), l = fmaf(hi_half(b.z), v[5], l);
+            l = fmaf(lo_half(b.w), v[6], l), l = fmaf(hi_half(b.w), v[7], l);
+          }
+          y = fmaf(a.lora_scale, l, y);
+        }
+        out = fmaf(gate[t], y, out);
+      }
     }
-    float y = y_of(TK + t);
-    if (a.shA[2]) {
-      float l = 0.f;
-      for (int k = 0; k < r; ++k) l = fmaf(half_bits_to_float(a.shB[2][static_cast<size_t>(hr) * r + k]), td[t * kMaxR + k], l);
-      y = fmaf(a.lora_scale, l, y);
-    }
-    v = fmaf(gate[t], y, v);
     const size_t at = static_cast<size_t>(t) * a.H + hr;
     if (a.out_mode == 1)
-      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(out);
     else if (a.out_mode == 2)
-      static_cast<float*>(a.out)[at] += v;
+      static_cast<float*>(a.out)[at] += out;
     else
-      static_cast<float*>(a.out)[at] = v;
+      static_cast<float*>(a.out)[at] = out;
   }
 }
 

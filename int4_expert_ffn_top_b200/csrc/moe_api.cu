@@ -1313,7 +1313,7 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
 namespace {
 
 struct LayerWs {
-  uint32_t* bar;
+  ld::Header* bar;
   uint8_t* img;
   float *us, *ic, *logits, *aux, *tgu, *tex;
   uint16_t* h;
@@ -1329,12 +1329,12 @@ LayerWs carve_layer(void* base, const moe_layer* L, int T, int K) {
     return base ? static_cast<char*>(base) + o : nullptr;
   };
   const size_t t = static_cast<size_t>(T), TK = t * K, r = L->r > 0 ? L->r : 0;
-  w.bar = reinterpret_cast<uint32_t*>(take(ld::kHeaderBytes));
+  w.bar = reinterpret_cast<ld::Header*>(take(ld::kHeaderBytes));
   w.img = reinterpret_cast<uint8_t*>(take(t * (2 * L->H + 16)));
   w.us = reinterpret_cast<float*>(take(t * (L->H / 64) * 4));
   w.ic = reinterpret_cast<float*>(take(t * 4));
   w.logits = reinterpret_cast<float*>(take(t * L->E * 4));
-  w.aux = reinterpret_cast<float*>(take(t * (1 + 2 * r) * 4));
+  w.aux = reinterpret_cast<float*>(take(t * (4 + 2 * r) * 4));
   w.h = reinterpret_cast<uint16_t*>(take((TK + t) * 2 * L->I * 2));
   w.tgu = reinterpret_cast<float*>(take(L->ex_lora_A_gu ? TK * 2 * r * 4 : 0));
   w.tex = reinterpret_cast<float*>(take(L->ex_lora_A ? TK * r * 4 : 0));
@@ -1344,7 +1344,7 @@ LayerWs carve_layer(void* base, const moe_layer* L, int T, int K) {
 
 // Shared-memory plan for a grid of `grid` CTAs; false if the shape does not fit.
 bool plan_layer(ld::Smem* s, const moe_layer* L, int T, int K, int grid, bool smem_image) {
-  const int H = L->H, I = L->I, G = H / 64, RGU = qrow_bytes(H, 4), RDN = qrow_bytes(I, 4);
+  const int H = L->H, G = H / 64;
   auto cdiv = [](int a, int b) { return (a + b - 1) / b; };
   size_t o = 0;
   auto put = [&](size_t n) {
@@ -1352,36 +1352,30 @@ bool plan_layer(ld::Smem* s, const moe_layer* L, int T, int K, int grid, bool sm
     o = at + n;
     return static_cast<int>(at);
   };
-  const int rows = cdiv(H, grid), nrt = cdiv(rows, ld::kDownRows), rt_rows = cdiv(rows, nrt);
-  const int nsp = cdiv(I, grid), nst = cdiv(nsp, 8);
-  const size_t y = static_cast<size_t>(T * K + T) * nrt * ld::kTileRows * 4;
-  s->img = smem_image ? put(static_cast<size_t>(T) * (2 * H + 16)) : 0;
-  s->us = put(static_cast<size_t>(T) * G * 4);
-  s->ic = put(T * 4);
-  s->scratch = put(y > 16384 ? y : 16384);
-  s->sraw = put(static_cast<size_t>(T) * 2 * nsp * 4);
+  const size_t t = static_cast<size_t>(T);
+  const int nrt = cdiv(cdiv(H, grid), ld::kDownRows), r = L->r > 0 ? L->r : 0;
+  size_t scratch = 2 * ld::kWarps * 32 * 16;  // partial sums of the gate/up teams; rows over all tokens: no more
+  const size_t y = (t * K + t) * nrt * 16 * 4, sh = static_cast<size_t>(cdiv(T, 8)) * (G / 4) * 512;
+  if (y > scratch) scratch = y;
+  if (sh > scratch) scratch = sh;
+  s->img = put(smem_image ? t * (2 * H + 16) : 0);
+  s->us = put(t * G * 4);
+  s->ic = put(t * 4);
+  s->scratch = put(scratch);
+  s->sraw = put(t * ld::kMaxSharedPairs * 8);
   s->sel = put(ld::kMaxSlots * 4);
   s->w = put(ld::kMaxSlots * 4);
   s->dist = put(ld::kMaxE * 4);
   s->start = put((ld::kMaxE + 1) * 4);
   s->slots = put(ld::kMaxSlots * 4);
   s->els = put(ld::kMaxEls * 4);
-  s->gate = put(T * 4);
-  s->td = put(static_cast<size_t>(T) * ld::kMaxR * 4);
+  s->gate = put(t * 4);
+  s->td = put((t > 96 ? t : 96) * ld::kMaxR * 4);  // partial sums of up to 24 (block, tile, part)s of 4 tokens
   s->red = put(2 * ld::kWarps * 8);
-  s->bars = put((2 * 8 + 4) * (ld::kMaxStagesG + ld::kMaxStagesD) + 96);
-  s->ring = put(0);
-  s->sg = ld::padded_row(RGU);
-  s->stage_g = ld::kTileRows * s->sg;
-  s->sd = ld::padded_row(RDN);
-  s->stage_d = ld::kDownRows * s->sd;
-  const int room = 227 * 1024 - s->ring;
-  if (room <= 0) return false;
-  s->nsg = room / s->stage_g < ld::kMaxStagesG ? room / s->stage_g : ld::kMaxStagesG;
-  s->nsd = room / s->stage_d < ld::kMaxStagesD ? room / s->stage_d : ld::kMaxStagesD;
-  const int g_bytes = s->nsg * s->stage_g, d_bytes = s->nsd * s->stage_d;
-  s->total = s->ring + (g_bytes > d_bytes ? g_bytes : d_bytes);
-  return s->nsg > nst && s->nsg >= 2 && s->nsd >= 2 && rt_rows <= ld::kDownRows;
+  s->misc = put(128);
+  s->ring = put(ld::kWarps * ld::kBuf * ld::kUnitBytes);
+  s->total = static_cast<int>(o);
+  return o <= 227 * 1024 && nrt <= 2 && cdiv(L->I, grid) <= ld::kMaxSharedPairs && cdiv(L->E + 1 + 2 * r, grid) <= 8;
 }
 
 // Multiprocessors of the current device, with the kernel's shared memory allowed there; 0 on failure.
@@ -1426,7 +1420,7 @@ moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, flo
   if (ws_bytes < ws.bytes) return MOE_ERR_WORKSPACE;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int grid = layer_grid();
-  if (grid < 64) return grid ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
+  if (grid < 1) return MOE_ERR_CUDA;
   ld::Args a{};
   a.T = T;
   a.K = K;
@@ -1434,6 +1428,9 @@ moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, flo
   a.H = L->H;
   a.I = L->I;
   while ((1 << a.logI) < L->I) ++a.logI;
+  while ((256 << a.logU) < L->H) ++a.logU;
+  a.gmul = static_cast<uint32_t>(((1ull << 32) + grid - 1) / grid);
+  a.kmul = (65536 + K - 1) / K;
   a.r = L->r;
   a.u = x ? nullptr : u;
   a.x = x;
@@ -1472,10 +1469,8 @@ moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, flo
   a.tex = ws.tex;
   a.err = err_word;
   a.timeout_ns = kGemmTimeoutNs;
-  a.smem_image = T * L->H <= 32768;
-  a.shared_build = !a.smem_image || (x && T > 4);
+  a.smem_image = T <= 4;
   if (!plan_layer(&a.sm, L, T, K, grid, a.smem_image)) return MOE_ERR_UNSUPPORTED;
-  if (cudaMemsetAsync(ws.bar, 0, ld::kHeaderBytes, st) != cudaSuccess) return MOE_ERR_CUDA;
   void* args[] = {&a};
   return cudaLaunchCooperativeKernel(reinterpret_cast<void*>(ld::layer_decode_kernel), dim3(grid), dim3(ld::kThreads),
                                      args, a.sm.total, st) == cudaSuccess

@@ -57,6 +57,7 @@ struct Args {
   const uint16_t* u;  // bf16 [T][H], or null: the normed x
   const float* x;     // fp32 [T][H] to norm, or null
   float eps;
+  double inv_h;  // 1 / H
   uint16_t* u_out;
   const int32_t* exec_idx;
   float* logits;
@@ -280,11 +281,13 @@ __device__ __noinline__ void build_image(const Args& a, int t, int wi, int warps
   if (warps > 1) {
     if (lane == 0) r[2 * wi] = ss, r[2 * wi + 1] = static_cast<double>(m);
     team_sync(team, warps);
-    ss = 0.0;
-#pragma unroll 4
-    for (int w = 0; w < warps; ++w) {
-      if (F32) ss += r[2 * w];
-      m = max_bits(m, static_cast<float>(r[2 * w + 1]));
+    const bool on = lane < warps;  // each warp adds up the others' sums, a lane per warp
+    m = on ? static_cast<float>(r[2 * lane + 1]) : 0.f;
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    if (F32) {
+      ss = on ? r[2 * lane] : 0.0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
   }
   float rstd = 1.f;
@@ -310,7 +313,14 @@ __device__ __noinline__ void build_image(const Args& a, int t, int wi, int warps
         for (int w = 0; w < warps; ++w) ss += r[2 * w];
       }
     }
-    rstd64 = 1.0 / sqrt(ss / a.H + static_cast<double>(a.eps));
+    const double v = ss * a.inv_h + static_cast<double>(a.eps);  // H is a power of two
+    if (v > 1e-30 && v < 1e30) {  // 1/sqrt(v): Newton's iteration from the fp32 value, 23 -> 46 -> 52 bits
+      double y = rsqrtf(static_cast<float>(v));
+      y = fma(0.5 * y, fma(-v * y, y, 1.0), y);
+      rstd64 = fma(0.5 * y, fma(-v * y, y, 1.0), y);
+    } else {
+      rstd64 = 1.0 / sqrt(v);
+    }
     rstd = static_cast<float>(rstd64);
     m = static_cast<float>(m * rstd64);
   }
@@ -457,19 +467,21 @@ MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* col, const float* u
 // Codes enter as code 2^-22 (and 16 times that).  The MMA aligns its products by their exponents, and a subnormal
 // counts with the smallest one, so two more of the mantissa's bits in use keep two more of h's 11 in the sum (u's 8 fit
 // either way): the result is off by 7e-7 of its size instead of 3e-6.
-MOE_DEV void down_unit(const uint8_t* buf, const uint8_t* col, bool whole, float (&acc)[4]) {
+MOE_DEV void down_unit(const uint8_t* buf, Frag f0, Frag f1, const uint8_t* col, bool whole, float (&acc)[4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const bool ones = g == 7;
   const uint8_t* ra = buf + g * kUnitRow;
   const uint8_t* rb = ones ? ra : ra + 8 * kUnitRow;
   const uint32_t lo = 0x003C003Cu, hi = 0x03C003C0u, one = 0x3C003C00u, sixteen = 0x4C004C00u;
+  Frag f2 = f0, f3 = f1;
+  if (whole) f2 = load_frag(col, 2), f3 = load_frag(col, 3);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h && !whole) break;  // a row of two groups
     float d[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const Frag f = load_frag(col, 2 * h + i);
+      const Frag& f = h ? (i ? f3 : f2) : (i ? f1 : f0);
       const uint2 wa = *reinterpret_cast<const uint2*>(ra + (2 * h + i) * 32 + tig * 8);
       const uint2 wb = *reinterpret_cast<const uint2*>(rb + (2 * h + i) * 32 + tig * 8);
       const uint32_t p0 = wa.x << 2, p1 = wa.x >> 6, p2 = wa.y << 2, p3 = wa.y >> 6;
@@ -564,6 +576,7 @@ __device__ __noinline__ void route_token(const Args& a, int t, int* sel, float* 
     key[i] = k;
   }
   int my_e = 0;
+  uint32_t my_k = 0;
 #pragma unroll 1
   for (int k = 0; k < K; ++k) {
     uint32_t best = key[0];
@@ -577,12 +590,18 @@ __device__ __noinline__ void route_token(const Args& a, int t, int* sel, float* 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (e == lane + 32 * i) key[i] = 0;
-    if (lane == k) my_e = min(e, a.E - 1);
+    if (lane == k) my_e = min(e, a.E - 1), my_k = top;
   }
   const bool write = blockIdx.x == 0;
   if (lane < K && write) a.idx[t * K + lane] = my_e;
   if (a.exec_idx && lane < K) my_e = min(max(a.exec_idx[t * K + lane], 0), a.E - 1);
-  const float l = lane < K ? __ldcg(lg + my_e) : -INFINITY;
+  float l = -INFINITY;
+  if (lane < K) {
+    if (a.exec_idx)
+      l = __ldcg(lg + my_e);
+    else  // the logit back from its key
+      l = my_k == 1u ? __uint_as_float(0x7fc00000u) : __uint_as_float(my_k ^ ((my_k >> 31) ? 0x80000000u : 0xffffffffu));
+  }
   float mx = l;
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -636,6 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   const int n8 = max(0, min(r1, a.E + 1) - r0);  // 8-bit rows r0 .. r0 + n8 - 1, then fp16 rows
   const int nblk = (T + 7) / 8;
 
+  if (tid == kThreads - 32) {
+    misc[0] = 0;
+    header_ready(a.bar, misc, a.err, a.timeout_ns);
+  }
   // --------------------------------------------------------------------------- weights that no token decides
   // The first shared tile's units: unit warp % U for token blocks warp / U, + sh_n, ...
   const uint32_t ring32 = sa(ring);
@@ -669,9 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     if (a.shA[1]) prefetch_l2(a.shB[1] + static_cast<size_t>(sp0 + tid) * r);
   }
   if (a.shA[2] && tid >= 32 && tid < 32 + ndr) prefetch_l2(a.shB[2] + static_cast<size_t>(dr0 + tid - 32) * r);
-  if (a.rbias && tid >= 64 && tid < 64 + n8 && r0 + tid - 64 < a.E) prefetch_l2(a.rbias + r0 + tid - 64);
-  if (tid == 0) misc[0] = 0;
-
+  const float bias = a.rbias && r0 + warp < min(r1, a.E) ? __ldg(a.rbias + r0 + warp) : 0.f;  // of row r0 + warp
   // --------------------------------------------------------------------------- token images
   const uint8_t* img = a.smem_image ? sm + S.img : a.img;
   float* us = reinterpret_cast<float*>(sm + S.us);
@@ -687,7 +708,6 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   if (!a.smem_image) {
     if (cta < T)
       build(cta, warp, kWarps, 0, a.img + static_cast<size_t>(cta) * ldu, a.us + cta * G, a.ic + cta, true);
-    if (tid == 0) header_ready(a.bar, failed, a.err, a.timeout_ns);
     grid_arrive(a.bar, B_IMAGE);
     grid_wait(a.bar, B_IMAGE, false, failed, a.err, a.timeout_ns);
 #pragma unroll 1
@@ -697,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     const int logW = T == 1 ? 4 : (T == 2 ? 3 : 2), W = 1 << logW, team = warp >> logW;  // at most 4 tokens
     if (team < T)
       build(team, warp & (W - 1), W, team, sm + S.img + team * ldu, us + team * G, ic + team, team == cta);
-    if (tid == 0) header_ready(a.bar, failed, a.err, a.timeout_ns);
   }
   named_sync(15, kThreads);
 
@@ -750,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
         v *= ic[t];
         const int j = first + q;
         if (j < a.E)
-          a.logits[static_cast<size_t>(t) * a.E + j] = v * 0x1p24f + (a.rbias ? __ldg(a.rbias + j) : 0.f);
+          a.logits[static_cast<size_t>(t) * a.E + j] = v * 0x1p24f + bias;  // kind 0: row r0 + warp
         else if (j == a.E)
           a.aux[t * (4 + 2 * r)] = v * 0x1p24f;
         else
@@ -808,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
 #pragma unroll 1
   for (int t = warp; t < T; t += kWarps) route_token(a, t, sel, sw, mask);
   float* gate = reinterpret_cast<float*>(sm + S.gate);
-  if (tid < T) gate[tid] = sigmoid(__ldcg(a.aux + tid * (4 + 2 * r)));
+  if (tid >= kThreads - 32 && lane < T) gate[lane] = sigmoid(__ldcg(a.aux + lane * (4 + 2 * r)));
   named_sync(15, kThreads);
   if (warp < 8) {  // chosen experts in ascending order, their slots in ascending order, the down elements
     int cnt = 0;
@@ -883,52 +902,73 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   }
 
   // --------------------------------------------------------------------------- chosen experts' gate/up
-  // The tiles (8 pairs) of all chosen experts, one after the other, are split evenly over the CTAs and there over teams
-  // of W warps; the W warps of a team split the units.  A warp's time goes by tiles x units; a team of more than one
-  // joins its sums at each tile, charged as one unit.
+  // The tiles (8 pairs) of all chosen experts, one after the other, are split evenly over the CTAs; a CTA's items (tile,
+  // block of 8 slots) are runs of U units each, and all its units are split evenly over the warps.  An item whose
+  // units fall to several warps is joined by the one that has its first unit, after a barrier: the others leave their
+  // sums in scratch (a warp has at most one item that it did not begin).
   {
-    const int logt = a.logI - 3, nt = D << logt, c0 = share(cta, nt, a.gmul), cn = share(cta + 1, nt, a.gmul) - c0;
-    int logW = 0, best = 1 << 30;
-#pragma unroll 1
-    for (int lw = 0; lw <= 3 && lw <= a.logU; ++lw) {
-      const int ts = kWarps >> lw, cost = ((cn + ts - 1) / ts) * ((U >> lw) + (lw > 0));
-      if (cost < best) best = cost, logW = lw;
-    }
-    const int W = 1 << logW, wi = warp & (W - 1), team = warp >> logW, ts = kWarps >> logW;
-    const int lo = c0 + team * cn / ts, hi = c0 + (team + 1) * cn / ts;
-    const int u0 = wi * (U >> logW), u1 = u0 + (U >> logW);
+    const int logt = a.logI - 3, nt = D << logt, t0 = share(cta, nt, a.gmul), t1 = share(cta + 1, nt, a.gmul);
     const int tmask = (1 << logt) - 1;
-    // the item being copied: base of its tile's records, and what follows it
-    int ipos = lo, ib = 0, iu = u0;
-    const uint8_t* ibase = nullptr;
-    auto open = [&]() {
-      ibase = a.pool + dist[ipos >> logt] * a.stride + static_cast<size_t>(16 * (ipos & tmask)) * RGU;
+    auto blocks = [&](int d) { return (start[d + 1] - start[d] + 7) >> 3; };
+    int items = 0;  // of this CTA
+#pragma unroll 1
+    for (int t = t0; t < t1;) {
+      const int d = t >> logt, e = min(t1, (d + 1) << logt);
+      items += (e - t) * blocks(d);
+      t = e;
+    }
+    const int total = items << a.logU;
+    auto border = [&](int w) { return static_cast<int>(static_cast<uint32_t>(total * w) / kWarps); };
+    const int ub = border(warp), ue = border(warp + 1);
+    struct At {  // a place in the CTA's run of units: tile, block of slots, unit
+      int t, b, u;
     };
-    if (lo < hi) open();
+    At at{t0, 0, ub & (U - 1)};
+    {
+      int i = ub >> a.logU;  // item of the first unit
+#pragma unroll 1
+      while (at.t < t1) {
+        const int d = at.t >> logt, e = min(t1, (d + 1) << logt), nb = blocks(d), n = (e - at.t) * nb;
+        if (i < n) {
+          const int q = nb == 1 ? i : i / nb;
+          at.t += q;
+          at.b = 8 * (i - q * nb);
+          break;
+        }
+        i -= n;
+        at.t = e;
+      }
+    }
+    At is = at;
+    int to_copy = ue - ub;
+    const uint8_t* ibase = nullptr;
+    auto open = [&]() { ibase = a.pool + dist[is.t >> logt] * a.stride + static_cast<size_t>(16 * (is.t & tmask)) * RGU; };
+    if (to_copy > 0) open();
     uint32_t wr = ring32;
-    const uint32_t ring_end = ring32 + kBuf * kUnitBytes;
     auto copy_next = [&]() {
-      if (ipos < hi) {
-        issue_unit(wr, plan, ibase + 128 * iu, ibase + 8 * iu, 8, 8);
-        if (++iu == u1) {
-          iu = u0;
-          ib += 8;
-          const int d = ipos >> logt;
-          if (ib >= start[d + 1] - start[d]) {
-            ib = 0;
-            if (++ipos < hi) open();
+      if (to_copy > 0) {
+        --to_copy;
+        issue_unit(wr, plan, ibase + 128 * is.u, ibase + 8 * is.u, 8, 8);
+        if (++is.u == U) {
+          is.u = 0;
+          is.b += 8;
+          const int d = is.t >> logt;
+          if (is.b >= start[d + 1] - start[d]) {
+            is.b = 0;
+            ++is.t;
+            if (to_copy > 0) open();
           }
         }
       }
       cp_commit();
-      if ((wr += kUnitBytes) == ring_end) wr = ring32;
+      if ((wr += kUnitBytes) == ring32 + kBuf * kUnitBytes) wr = ring32;
     };
 #pragma unroll 1
     for (int i = 0; i < kBuf - 1; ++i) copy_next();
 
     // the shared expert's hidden values while the first copies are under way: a pair of lanes per (token, pair)
 #pragma unroll 1
-    for (int t = warp; t < T && nsp > 0; t += kWarps) {
+    for (int t = kWarps - 1 - warp; t < T && nsp > 0; t += kWarps) {
       const int pr = min(lane >> 1, nsp - 1), up = lane & 1;
       const float2 v = reinterpret_cast<const float2*>(sraw)[t * 16 + pr];
       float x = up ? v.y : v.x;
@@ -941,68 +981,81 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     }
 
     uint8_t* rd = ring;
-    int pos = lo, b = 0, u = u0, flip = 0;
     int d = 0, s0 = 0, cnt = 0;
     const uint8_t* col = nullptr;
-    const float *ua = nullptr, *ub = nullptr;
-    auto columns = [&]() {  // of item (pos, b)
-      d = pos >> logt;
+    const float *ua = nullptr, *uc = nullptr;
+    auto columns = [&]() {  // of item (at.t, at.b)
+      d = at.t >> logt;
       s0 = start[d];
       cnt = start[d + 1] - s0;
-      const int c0 = s0 + b, cl = s0 + cnt - 1;
+      const int c0 = s0 + at.b, cl = s0 + cnt - 1;
       col = img + static_cast<size_t>(slots[min(c0 + g, cl)] >> 16) * ldu;
       ua = us + (slots[min(c0 + 2 * tig, cl)] >> 16) * G;
-      ub = us + (slots[min(c0 + 2 * tig + 1, cl)] >> 16) * G;
+      uc = us + (slots[min(c0 + 2 * tig + 1, cl)] >> 16) * G;
     };
+    float4* part = reinterpret_cast<float4*>(scratch);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (lo < hi) columns();
+    bool mine = at.u == 0;
+    auto finish = [&]() {  // hidden values of item (at.t, at.b)
+      const int j = (at.t & tmask) * 8 + g;
 #pragma unroll 1
-    while (pos < hi) {
-      copy_next();
-      cp_wait<kBuf - 1>();
-      gate_up_unit(rd, col + u * 512, ua + 4 * u, ub + 4 * u, acc);
-      if ((rd += kUnitBytes) == ring + kBuf * kUnitBytes) rd = ring;
-      if (++u == u1) {
-        u = u0;
-        bool mine = true;
-        if (W > 1) {  // the team's first warp adds up; the two buffers take turns, so one barrier a tile does
-          float4* p = reinterpret_cast<float4*>(scratch) + flip * (kWarps * 32);
-          p[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          flip ^= 1;
-          team_sync(team, W);
-          mine = wi == 0;
-          if (mine) {
-#pragma unroll 1
-            for (int w = 1; w < W; ++w) {
-              const float4 v = p[(warp + w) * 32 + lane];
-              acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
-            }
-          }
+      for (int c = 0; c < 2; ++c) {
+        const int q = s0 + at.b + 2 * tig + c;
+        if (q >= s0 + cnt) break;
+        const int sl = slots[q] & 0xffff;
+        const float k = ic[slots[q] >> 16] * 0x1p24f;
+        float x = (c ? acc[1] : acc[0]) * k, y = (c ? acc[3] : acc[2]) * k;
+        if (a.exAgu) {
+          const uint16_t* B = a.exBgu + (static_cast<size_t>(dist[d]) * 2 * a.I + 2 * j) * r;
+          const float* t = a.tgu + static_cast<size_t>(sl) * 2 * r;
+          x = fmaf(a.lora_scale, dot_r(B, t, r), x);
+          y = fmaf(a.lora_scale, dot_r(B + r, t + r, r), y);
         }
-        if (mine) {
-          const int j = (pos & tmask) * 8 + g;
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            const int q = 2 * tig + c;
-            if (b + q >= cnt) break;
-            const int sl = slots[s0 + b + q] & 0xffff;
-            const float k = ic[slots[s0 + b + q] >> 16] * 0x1p24f;
-            float x = (c ? acc[1] : acc[0]) * k, y = (c ? acc[3] : acc[2]) * k;
-            if (a.exAgu) {
-              const uint16_t* B = a.exBgu + (static_cast<size_t>(dist[d]) * 2 * a.I + 2 * j) * r;
-              const float* t = a.tgu + static_cast<size_t>(sl) * 2 * r;
-              x = fmaf(a.lora_scale, dot_r(B, t, r), x);
-              y = fmaf(a.lora_scale, dot_r(B + r, t + r, r), y);
-            }
-            store_h(a, sl, j, x, y);
-          }
-        }
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        b += 8;
-        if (b >= cnt) b = 0, ++pos;
-        if (pos < hi) columns();
+        store_h(a, sl, j, x, y);
       }
       __syncwarp();
+    };
+    int i = ub;
+    if (ub < ue) columns();
+    // one more turn after the last unit: the barrier, and the item that the warp began and others went on with
+#pragma unroll 1
+    for (;;) {
+      bool whole = false;
+      if (i < ue) {
+        copy_next();
+        cp_wait<kBuf - 1>();
+        gate_up_unit(rd, col + at.u * 512, ua + 4 * at.u, uc + 4 * at.u, acc);
+        if ((rd += kUnitBytes) == ring + kBuf * kUnitBytes) rd = ring;
+        __syncwarp();
+        ++i;
+        whole = ++at.u == U;
+        if (!whole && i < ue) continue;
+        if (!mine) {
+          part[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        }
+      } else {
+        if (ub == ue) part[warp * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+        named_sync(15, kThreads);
+        if (ub == ue || !mine || at.u == 0) break;
+        const int end = ue + U - at.u;  // of the item
+#pragma unroll 2
+        for (int w = warp + 1; w < kWarps && border(w) < end; ++w) {
+          const float4 v = part[w * 32 + lane];
+          acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+        }
+        whole = true;
+      }
+      if (whole) {
+        if (mine) finish();
+        if (i >= ue && at.u != U) break;  // joined
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        mine = true;
+        at.u = 0;
+        at.b += 8;
+        if (at.b >= cnt) at.b = 0, ++at.t;
+        if (i < ue) columns();
+      }
     }
   }
   grid_arrive(a.bar, B_HIDDEN);
@@ -1041,6 +1094,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   cp_wait<0>();
 #pragma unroll 1
   for (int i = 0; i < kBuf - 1; ++i) copy_next();
+  if (a.shA[2] && warp < ndr && lane < (r * 2 + 127) / 128)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(a.shB[2] + static_cast<size_t>(dr0 + warp) * r + 64 * lane));
   grid_wait(a.bar, B_HIDDEN, !a.exA, failed, a.err, a.timeout_ns);
 
   const uint8_t* hb = reinterpret_cast<const uint8_t*>(a.h);
@@ -1088,9 +1143,10 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     while (i < total) {
+      const Frag f0 = load_frag(col + u * 512, 0), f1 = load_frag(col + u * 512, 1);
       copy_next();
       cp_wait<kBuf - 1>();
-      down_unit(rd, col + u * 512, G2 >= 4, acc);
+      down_unit(rd, f0, f1, col + u * 512, G2 >= 4, acc);
       if ((rd += kUnitBytes) == ring + kBuf * kUnitBytes) rd = ring;
       if (++u == u1) {
         u = u0;

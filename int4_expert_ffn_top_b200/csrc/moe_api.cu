@@ -1435,6 +1435,7 @@ moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, flo
   a.u = x ? nullptr : u;
   a.x = x;
   a.eps = eps;
+  a.inv_h = 1.0 / L->H;
   a.u_out = x ? u : nullptr;
   a.exec_idx = exec_idx;
   a.logits = logits ? logits : ws.logits;

@@ -8,7 +8,7 @@
 // goes into the scale alone, so the quantiser never forms the normed row.
 #pragma once
 
-#include "common.cuh"
+#include "tc_primitives.cuh"
 
 namespace moe {
 namespace l8 {
@@ -103,8 +103,7 @@ MOE_DEV void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t
 }
 
 MOE_DEV void store_out(const LinArgs& a, int t, int n, int acc) {
-  float y = static_cast<float>(acc) * a.sx[t] * a.sw[n];
-  if (a.bias) y += a.bias[n];
+  const float y = fmaf(static_cast<float>(acc) * a.sx[t], a.sw[n], a.bias ? a.bias[n] : 0.f);
   const size_t o = static_cast<size_t>(t) * a.N + n;
   if (a.out_mode == 1) {
     static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
@@ -164,6 +163,212 @@ __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, i
     int v = 0;
     for (int w = 0; w < KW; ++w) v += part[tl * KW + w][t][r];
     store_out(a, t0 + t, n, v);
+  }
+}
+
+// ----------------------------------------------------------------------------- many tokens: tcgen05 kind::i8
+// D[n][t] = sum_k W[n][k] q[t][k]: 128 weight rows are the MMA's M side, BN tokens its N side, 32-bit integer
+// accumulators in tensor memory.  Persistent and warp-specialised: warp 0 brings 128-byte K slices of both operands by
+// TMA (128-byte swizzle, kStages of them, zero-filled past the matrices' edges), warp 1 issues the MMAs (four k32 steps a
+// slice), eight epilogue warps (TMEM lane quadrant = warp % 4, two warps per quadrant splitting the columns) drain one
+// accumulator while the next tile's MMAs fill the other.  A lane is a weight row and a column a token, so the 32 lanes
+// of a store write 32 neighbouring outputs of one token.
+// Every wait is bounded: a role whose wait runs out stops and records MOE_ERR_TIMEOUT; copies and MMAs under way are
+// waited for (bounded) before the CTA leaves.
+constexpr int kGM = 128, kGK = 128;
+constexpr int kGEpiWarps = 8, kGThreads = 64 + 32 * kGEpiWarps;
+
+template <int BN>
+struct GemmCfg {
+  static constexpr int kStage = (kGM + BN) * kGK;
+  static constexpr int kStages = BN >= 256 ? 4 : (BN >= 192 ? 5 : (BN >= 128 ? 6 : 8));
+  static constexpr int kSxBytes = 2 * BN * 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kSxBytes + 256;
+  static constexpr uint32_t kCols = 2 * BN <= 64 ? 64 : (2 * BN <= 128 ? 128 : (2 * BN <= 256 ? 256 : 512));
+};
+
+struct GemmMaps {
+  CUtensorMap w, q;
+};
+
+struct GemmArgs {
+  LinArgs lin;
+  int KT, m_tiles, n_tiles;  // K slices; tiles of weight rows, of tokens
+  int* err;
+  long long timeout_ns;
+};
+
+// Instruction descriptor, kind::i8: signed 8-bit A and B (K-major), 32-bit integer accumulator, M = 128, N = n.
+MOE_DEV uint32_t instr_desc_i8(int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+MOE_DEV void mma_i8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// OR of v over the 256 epilogue threads (named barrier 1).
+MOE_DEV bool epi_any(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
+template <int BN, int MODE>
+__global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constant__ GemmMaps maps,
+                                                            const __grid_constant__ GemmArgs a) {
+  using C = GemmCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* sxs = reinterpret_cast<float*>(sm + C::kStages * C::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kStages * C::kStage + C::kSxBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = a.m_tiles * a.n_tiles;
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      tc::bar_init(full + s, 1);
+      tc::bar_init(empty + s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::bar_init(acc_full + s, 1);
+      tc::bar_init(acc_empty + s, kGEpiWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::sa(tmem_slot)),
+                 "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+  int fail = 0;
+  auto parity = [](int i, int n) { return static_cast<uint32_t>(i / n) & 1u; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int n = 0;
+#pragma unroll 1
+      for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x) {
+        const int m0 = (t % a.m_tiles) * kGM, t0 = (t / a.m_tiles) * BN;
+#pragma unroll 1
+        for (int k = 0; k < a.KT; ++k, ++n) {
+          const int s = n % C::kStages;
+          if (!tc::bar_wait(empty + s, parity(n, C::kStages) ^ 1u, a.timeout_ns)) {
+            fail = 1;
+            break;
+          }
+          tc::bar_expect_tx(full + s, C::kStage);
+          tc::tma_load_2d(sm + s * C::kStage, &maps.w, k * kGK, m0, full + s);
+          tc::tma_load_2d(sm + s * C::kStage + kGM * kGK, &maps.q, k * kGK, t0, full + s);
+        }
+      }
+#pragma unroll 1
+      for (int q = n > C::kStages ? n - C::kStages : 0; fail && q < n; ++q)  // copies under way
+        tc::bar_wait(full + q % C::kStages, parity(q, C::kStages), a.timeout_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = instr_desc_i8(BN);
+      int n = 0, it = 0;
+#pragma unroll 1
+      for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x, ++it) {
+        const int ab = it & 1;
+        if (!tc::bar_wait(acc_empty + ab, parity(it, 2) ^ 1u, a.timeout_ns)) {
+          fail = 1;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t d = tmem + ab * BN;
+#pragma unroll 1
+        for (int k = 0; k < a.KT; ++k, ++n) {
+          const int s = n % C::kStages;
+          if (!tc::bar_wait(full + s, parity(n, C::kStages), a.timeout_ns)) {
+            fail = 1;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t da = tc::smem_desc(tc::sa(sm + s * C::kStage)), db = tc::smem_desc(tc::sa(sm + s * C::kStage + kGM * kGK));
+#pragma unroll
+          for (int i = 0; i < kGK / 32; ++i) mma_i8(d, da + 2 * i, db + 2 * i, idesc, k > 0 || i > 0);
+          tc::mma_commit(empty + s);
+        }
+        if (!fail) tc::mma_commit(acc_full + ab);
+      }
+      if (fail && n > 0) {  // MMAs under way
+        const int q = n - 1;
+        tc::bar_wait(empty + q % C::kStages, parity(q, C::kStages), a.timeout_ns);
+      }
+    }
+  } else {
+    const int ew = warp - 2, quad = warp & 3, half = ew >> 2, et = tid - 64;
+    int it = 0;
+#pragma unroll 1
+    for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x, ++it) {
+      const int ab = it & 1, m0 = (t % a.m_tiles) * kGM, t0 = (t / a.m_tiles) * BN;
+      const int n = m0 + quad * 32 + lane;
+      const bool row = n < a.lin.N;
+      const float sw = row ? __ldg(a.lin.sw + n) : 0.f, bias = row && a.lin.bias ? __ldg(a.lin.bias + n) : 0.f;
+      float* sx = sxs + ab * BN;
+#pragma unroll 1
+      for (int i = et; i < BN; i += 32 * kGEpiWarps) sx[i] = t0 + i < a.lin.T ? __ldg(a.lin.sx + t0 + i) : 0.f;
+      // the eight warps go on together or not at all (and see the scales)
+      if (epi_any(!tc::bar_wait(acc_full + ab, parity(it, 2), a.timeout_ns))) {
+        fail = 1;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+      for (int c = half * 32; c < BN && t0 + c < a.lin.T; c += 64) {
+        float v[32];
+        tc::tmem_ld32(tmem + ab * BN + c + (static_cast<uint32_t>(quad * 32) << 16), v);
+        if (c + 64 >= BN || t0 + c + 64 >= a.lin.T) {  // this warp's last read of the accumulator
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(acc_empty + ab);
+        }
+        const size_t base = static_cast<size_t>(t0 + c) * a.lin.N + n;
+        const int cols = min(32, a.lin.T - t0 - c);
+        if (row) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (i < cols) {
+              const float y = fmaf(static_cast<float>(__float_as_int(v[i])) * sx[c + i], sw, bias);
+              const size_t o = base + static_cast<size_t>(i) * a.lin.N;
+              if (MODE == 1) {
+                static_cast<__nv_bfloat16*>(a.lin.out)[o] = __float2bfloat16_rn(y);
+              } else {
+                float* p = static_cast<float*>(a.lin.out) + o;
+                *p = MODE == 2 ? *p + y : y;
+              }
+            }
+          }
+        }
+      }
+      if (!(half * 32 < BN && t0 + half * 32 < a.lin.T)) {  // nothing to read for this warp
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(acc_empty + ab);
+      }
+    }
+  }
+  if (fail) report(a.err, 5 /* MOE_ERR_TIMEOUT */);
+  __syncthreads();
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
   }
 }
 

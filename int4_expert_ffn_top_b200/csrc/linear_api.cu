@@ -1,6 +1,7 @@
 // C ABI of the 8-bit integer matrix product and its quantiser: host checks and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -28,6 +29,84 @@ void launch_rows(const l8::LinArgs& a, cudaStream_t st) {
   const int per = l8::kRowWarps / kw;
   dim3 grid((tiles + per - 1) / per, (a.T + NT * 8 - 1) / (NT * 8));
   l8::rows_kernel<NT><<<grid, 32 * l8::kRowWarps, 0, st>>>(a, kw);
+}
+
+constexpr int kMaxDev = 64;
+
+// Multiprocessors of the current device (0 on failure) and its number.
+int multiprocessors(int* dev) {
+  static std::atomic<int> known[kMaxDev];
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDev) return 0;
+  int n = known[*dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess) return 0;
+    known[*dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiledFn>(nullptr);
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// A matrix of `rows` rows of `cols` bytes, ld bytes apart, in boxes of 128 bytes x box_rows, 128-byte swizzle; what a
+// box has past the edges is zero.
+bool codes_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t ld, int box_rows) {
+  const EncodeTiledFn f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {l8::kGK, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, int MODE>
+moe_status launch_gemm_mode(const l8::GemmMaps& maps, const l8::GemmArgs& a, int nsm, int dev, cudaStream_t st) {
+  auto kern = l8::gemm_kernel<BN, MODE>;
+  static std::atomic<bool> allowed[kMaxDev];
+  if (!allowed[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, l8::GemmCfg<BN>::kSmem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    allowed[dev].store(true, std::memory_order_relaxed);
+  }
+  const int tiles = a.m_tiles * a.n_tiles;
+  kern<<<tiles < nsm ? tiles : nsm, l8::kGThreads, l8::GemmCfg<BN>::kSmem, st>>>(maps, a);
+  return launched();
+}
+
+template <int BN>
+moe_status launch_gemm(const l8::LinArgs& lin, int in_dim, int* err, int nsm, int dev, cudaStream_t st) {
+  l8::GemmMaps maps;
+  if (!codes_map(&maps.w, lin.W, in_dim, lin.N, lin.ldw, l8::kGM) ||
+      !codes_map(&maps.q, lin.q, in_dim, lin.T, lin.ldq, BN))
+    return MOE_ERR_CUDA;
+  l8::GemmArgs a{};
+  a.lin = lin;
+  a.KT = (in_dim + l8::kGK - 1) / l8::kGK;
+  a.m_tiles = (lin.N + l8::kGM - 1) / l8::kGM;
+  a.n_tiles = (lin.T + BN - 1) / BN;
+  a.err = err;
+  a.timeout_ns = 2000000000LL;
+  switch (lin.out_mode) {
+    case 0: return launch_gemm_mode<BN, 0>(maps, a, nsm, dev, st);
+    case 1: return launch_gemm_mode<BN, 1>(maps, a, nsm, dev, st);
+    default: return launch_gemm_mode<BN, 2>(maps, a, nsm, dev, st);
+  }
 }
 
 }  // namespace
@@ -82,9 +161,23 @@ moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, con
     launch_rows<2>(a, st);
   else if (T <= 32)
     launch_rows<4>(a, st);
-  else
+  else if (T <= 64)
     launch_rows<8>(a, st);
-  (void)err_word;
+  else {
+    int dev = 0;
+    const int nsm = multiprocessors(&dev);
+    if (nsm < 1) return MOE_ERR_CUDA;
+    // the token tile whose waves of tiles take the least time: a tile costs its columns, and 16 more for its turn
+    auto cost = [&](int bn) {
+      const long long tiles = static_cast<long long>((a.N + l8::kGM - 1) / l8::kGM) * ((T + bn - 1) / bn);
+      return (tiles + nsm - 1) / nsm * (bn + 16);
+    };
+    const long long c256 = cost(256), c192 = cost(192), c128 = cost(128), c64 = cost(64);
+    if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_gemm<256>(a, W->in_dim, err_word, nsm, dev, st);
+    if (c192 <= c128 && c192 <= c64) return launch_gemm<192>(a, W->in_dim, err_word, nsm, dev, st);
+    if (c128 <= c64) return launch_gemm<128>(a, W->in_dim, err_word, nsm, dev, st);
+    return launch_gemm<64>(a, W->in_dim, err_word, nsm, dev, st);
+  }
   return launched();
 }
 

@@ -40,29 +40,70 @@ struct QuantArgs {
   float* scale;
 };
 
-template <bool BF16>
-MOE_DEV float load1(const void* x, size_t i) {
-  if (BF16) return bf16_bits_to_float(static_cast<const uint16_t*>(x)[i]);
-  return static_cast<const float*>(x)[i];
-}
+// A kernel that runs after the quantiser in a stream may start while it runs (programmatic launch): it reads the weights
+// early, and the codes, the scales and its output only after dependency_wait().
+MOE_DEV void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+MOE_DEV void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// One block per token.
-template <bool BF16>
-__global__ void __launch_bounds__(kQThreads) quant_kernel(const QuantArgs a) {
-  __shared__ float red[2][kQThreads / 32];
-  const int t = blockIdx.x, tid = threadIdx.x;
-  const size_t row = static_cast<size_t>(t) * a.H;
-  float m = 0.f, ss = 0.f;
-  for (int i = tid; i < a.H; i += kQThreads) {
-    const float v = load1<BF16>(a.x, row + i);
-    m = max_bits(m, fabsf(v));
-    ss = fmaf(v, v, ss);
-  }
+// Eight neighbouring values of a row, or (VEC false: rows that are not aligned or not whole blocks) one.
+template <bool BF16, bool VEC>
+struct Piece {
+  static constexpr int kN = VEC ? 8 : 1;
+  float v[kN];
+  MOE_DEV void load(const void* x, size_t i) {
+    if (VEC && BF16) {
+      const uint4 p = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i);
+      const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    m = max_bits(m, __shfl_xor_sync(0xffffffffu, m, o));
-    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      for (int j = 0; j < kN; ++j) v[j] = __uint_as_float((j & 1) ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+    } else if (VEC) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 p = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + i + 4 * h);
+        const float q[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[(4 * h + j) % kN] = q[j];
+      }
+    } else {
+      v[0] = BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
+    }
   }
+};
+
+// One block per token; a thread keeps its first kKeep pieces in registers between the two passes.  Bound by memory:
+// 3,328 x 2,048 fp32 (34 MB in and out) takes 8.4 us with the launch.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kQThreads) quant_kernel(const QuantArgs a) {
+  using P = Piece<BF16, VEC>;
+  constexpr int kKeep = VEC ? 2 : 4;
+  __shared__ float red[2][kQThreads / 32];
+  dependents_may_start();
+  const int t = blockIdx.x, tid = threadIdx.x, n = a.H / P::kN;
+  const size_t row = static_cast<size_t>(t) * a.H;
+  P keep[kKeep];
+  float m = 0.f, ss = 0.f;
+  auto take = [&](const P& p) {
+#pragma unroll
+    for (int j = 0; j < P::kN; ++j) {
+      m = max_bits(m, fabsf(p.v[j]));
+      ss = fmaf(p.v[j], p.v[j], ss);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (tid + i * kQThreads < n) keep[i].load(a.x, row + static_cast<size_t>(tid + i * kQThreads) * P::kN);
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (tid + i * kQThreads < n) take(keep[i]);
+#pragma unroll 2
+  for (int i = tid + kKeep * kQThreads; i < n; i += kQThreads) {
+    P p;
+    p.load(a.x, row + static_cast<size_t>(i) * P::kN);
+    take(p);
+  }
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if ((tid & 31) == 0) red[0][tid >> 5] = m, red[1][tid >> 5] = ss;
   __syncthreads();
   m = red[0][0], ss = red[1][0];
@@ -71,9 +112,29 @@ __global__ void __launch_bounds__(kQThreads) quant_kernel(const QuantArgs a) {
   const bool fine = m <= 3.402823466e38f;  // false for infinity and NaN
   const float c = m < 1e-20f ? 0x1p64f : (m > 1e20f ? 0x1p-64f : 1.f);  // exact; keeps 127/m and x k in range
   const float mc = m * c, k = m > 0.f ? 127.f / mc : 0.f;
+  const bool zero = !fine || m == 0.f;
   int8_t* out = a.q + static_cast<size_t>(t) * a.ldq;
-  for (int i = tid; i < a.H; i += kQThreads)
-    out[i] = static_cast<int8_t>(fine && m > 0.f ? code_of(load1<BF16>(a.x, row + i) * c, mc, k) : 0);
+  auto put = [&](const P& p, int i) {
+    uint32_t w[2] = {0u, 0u};
+    if (!zero) {
+#pragma unroll
+      for (int j = 0; j < P::kN; ++j)
+        w[j >> 2] |= (static_cast<uint32_t>(code_of(p.v[j] * c, mc, k)) & 0xffu) << (8 * (j & 3));
+    }
+    if (VEC)
+      *reinterpret_cast<uint2*>(out + static_cast<size_t>(i) * 8) = make_uint2(w[0], w[1]);
+    else
+      out[i] = static_cast<int8_t>(w[0]);
+  };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (tid + i * kQThreads < n) put(keep[i], tid + i * kQThreads);
+#pragma unroll 1
+  for (int i = tid + kKeep * kQThreads; i < n; i += kQThreads) {
+    P p;
+    p.load(a.x, row + static_cast<size_t>(i) * P::kN);
+    put(p, i);
+  }
   if (tid == 0) {
     float s = m / 127.f;
     if (a.eps >= 0.f && m > 0.f) s = m * (1.f / sqrtf(ss / static_cast<float>(a.H) + a.eps)) / 127.f;
@@ -95,13 +156,6 @@ struct LinArgs {
   int out_mode;
 };
 
-MOE_DEV void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 MOE_DEV void store_out(const LinArgs& a, int t, int n, int acc) {
   const float y = fmaf(static_cast<float>(acc) * a.sx[t], a.sw[n], a.bias ? a.bias[n] : 0.f);
   const size_t o = static_cast<size_t>(t) * a.N + n;
@@ -115,54 +169,73 @@ MOE_DEV void store_out(const LinArgs& a, int t, int n, int acc) {
 
 constexpr int kRowWarps = 8;
 
-// Few tokens: the weight rows are the MMA's M side (16 rows a warp, read once from memory straight into the
-// fragments), 8 NT tokens its N side.  A lane's 16 bytes of a row are two k32 slices' fragments: K is permuted
-// the same way in both operands, which leaves the integer sum as it is.  KW warps split K and add up in shared
-// memory, so that enough loads are in flight when there are few rows.
-template <int NT>
+// Few tokens: a warp takes R weight rows, a lane every 32nd 16-byte chunk of them (of its part of K: KW warps split it
+// and add up in shared memory, so that enough loads are in flight when there are few rows), four dp4a a chunk, row and
+// token.  Bound by the weights' bytes; the tensor cores would add nothing to them (mma.sync s8, tried first, has its own
+// limit here: 27.7 us against xx for one token x 2,048 -> 65,536).
+template <int R, int NT>
 __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, int KW) {
-  __shared__ int part[kRowWarps][NT * 8][17];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tig = lane & 3;
-  const int tiles = kRowWarps / KW, tile = warp / KW, kw = warp % KW;
-  const int n0 = (blockIdx.x * tiles + tile) * 16, t0 = blockIdx.y * NT * 8;
-  int acc[NT][4];
+  __shared__ int part[kRowWarps][R * NT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = kRowWarps / KW, grp = warp / KW, kw = warp % KW;
+  const int n0 = (blockIdx.x * groups + grp) * R;
+  const int8_t* w[R];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int i = 0; i < R; ++i) w[i] = a.W + static_cast<size_t>(min(n0 + i, a.N - 1)) * a.ldw;
+  int acc[R][NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0;
-  if (n0 < a.N) {
-    const int8_t* w0 = a.W + static_cast<size_t>(min(n0 + g, a.N - 1)) * a.ldw;
-    const int8_t* w1 = a.W + static_cast<size_t>(min(n0 + g + 8, a.N - 1)) * a.ldw;
-    const int8_t* x[NT];
+  for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) x[j] = a.q + static_cast<size_t>(min(t0 + j * 8 + g, a.T - 1)) * a.ldq;
-    const int steps = (a.K16 + 3) / 4;  // of 64 bytes
-#pragma unroll 4
-    for (int s = kw; s < steps; s += KW) {
-      const int c = s * 4 + tig;
-      const bool in = c < a.K16;
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      const uint4 p = in ? ldg_stream(w0 + 16 * c) : z, q = in ? ldg_stream(w1 + 16 * c) : z;
+    for (int t = 0; t < NT; ++t) acc[i][t] = 0;
+  constexpr int kAhead = 16 / R;  // chunks whose weights are loaded together
+  bool waited = false;
+#pragma unroll 1
+  for (int c0 = kw * 32 + lane; c0 - lane < a.K16; c0 += 32 * KW * kAhead) {
+    uint4 q[kAhead][R];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint4 b = in ? *reinterpret_cast<const uint4*>(x[j] + 16 * c) : z;
-        mma_s8(acc[j], p.x, q.x, p.y, q.y, b.x, b.y);
-        mma_s8(acc[j], p.z, q.z, p.w, q.w, b.z, b.w);
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int c = c0 + j * 32 * KW;
+        q[j][i] = c < a.K16 ? ldg_stream(w[i] + 16 * static_cast<size_t>(c)) : make_uint4(0, 0, 0, 0);
+      }
+    if (!waited) {
+      dependency_wait();
+      waited = true;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = min(c0 + j * 32 * KW, a.K16 - 1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint4 x = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(min(t, a.T - 1)) * a.ldq + 16 * static_cast<size_t>(c));
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          int s = acc[i][t];
+          s = __dp4a(static_cast<int>(q[j][i].x), static_cast<int>(x.x), s);
+          s = __dp4a(static_cast<int>(q[j][i].y), static_cast<int>(x.y), s);
+          s = __dp4a(static_cast<int>(q[j][i].z), static_cast<int>(x.z), s);
+          acc[i][t] = __dp4a(static_cast<int>(q[j][i].w), static_cast<int>(x.w), s);
+        }
       }
     }
   }
+  if (!waited) dependency_wait();
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[warp][j * 8 + 2 * tig + (i & 1)][g + 8 * (i >> 1)] = acc[j][i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < tiles * NT * 8 * 16; i += 32 * kRowWarps) {
-    const int r = i & 15, t = (i >> 4) % (NT * 8), tl = i / (16 * NT * 8);
-    const int n = (blockIdx.x * tiles + tl) * 16 + r;
-    if (n >= a.N || t0 + t >= a.T) continue;
+    for (int t = 0; t < NT; ++t) {
+      const int v = __reduce_add_sync(0xffffffffu, acc[i][t]);
+      if (lane == (i * NT + t) % 32) part[warp][i * NT + t] = v;
+    }
+  if (KW > 1)
+    __syncthreads();
+  else
+    __syncwarp();
+  if (kw == 0 && lane < R * NT) {
+    const int i = lane / NT, t = lane % NT, n = n0 + i;
     int v = 0;
-    for (int w = 0; w < KW; ++w) v += part[tl * KW + w][t][r];
-    store_out(a, t0 + t, n, v);
+    for (int k = 0; k < KW; ++k) v += part[warp + k][lane];
+    if (n < a.N && t < a.T) store_out(a, t, n, v);
   }
 }
 
@@ -260,6 +333,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
 
   if (warp == 0) {
     if (lane == 0) {
+      dependency_wait();
       int n = 0;
 #pragma unroll 1
       for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x) {
@@ -315,6 +389,7 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
     }
   } else {
     const int ew = warp - 2, quad = warp & 3, half = ew >> 2, et = tid - 64;
+    dependency_wait();
     int it = 0;
 #pragma unroll 1
     for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x, ++it) {
@@ -369,6 +444,157 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+  }
+}
+
+// ----------------------------------------------------------------------------- a medium number of tokens: K split over a cluster
+// The same product where the tiles are too few for the device: the CTAs of a cluster take a run of K slices each (all of
+// a CTA's slices, or kSplitStages of them, are under way at once), leave their integer sums in shared memory, and each
+// CTA adds up and writes its part of the columns, reading its neighbours' sums through distributed shared memory.
+// Integer sums: the split leaves no trace in the result.
+constexpr int kSplitStages = 4, kSplitThreads = 192;
+
+template <int BN>
+struct SplitCfg {
+  static constexpr int kStage = (kGM + BN) * kGK;
+  static constexpr int kSmem = 1024 + kSplitStages * kStage + 256;
+  static_assert(kSplitStages * kStage >= BN * kGM * 4, "the sums fit where the operands were");
+};
+
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+template <int BN, int MODE>
+__global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_constant__ GemmMaps maps,
+                                                                 const __grid_constant__ GemmArgs a, int S) {
+  using C = SplitCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kSplitStages * C::kStage);
+  uint64_t* empty = full + kSplitStages;
+  uint64_t* done = empty + kSplitStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % S, m0 = (blockIdx.x / S) * kGM, t0 = blockIdx.y * BN;  // clusters run along x
+  const int k0 = rank * a.KT / S, k1 = (rank + 1) * a.KT / S;
+  if (tid == 0) {
+    for (int s = 0; s < kSplitStages; ++s) {
+      tc::bar_init(full + s, 1);
+      tc::bar_init(empty + s, 1);
+    }
+    tc::bar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::sa(tmem_slot)), "r"(BN));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+  int fail = 0;
+  auto parity = [](int i) { return static_cast<uint32_t>(i / kSplitStages) & 1u; };
+  if (warp == 0 && lane == 0) {
+    // the first slices' weights do not wait for the codes
+    const int first = min(k1 - k0, kSplitStages);
+#pragma unroll 1
+    for (int n = 0; n < first; ++n) {
+      tc::bar_expect_tx(full + n, C::kStage);
+      tc::tma_load_2d(sm + n * C::kStage, &maps.w, (k0 + n) * kGK, m0, full + n);
+    }
+    dependency_wait();
+    int n = 0;
+#pragma unroll 1
+    for (; n < k1 - k0; ++n) {
+      const int s = n % kSplitStages;
+      if (n >= kSplitStages) {
+        if (!tc::bar_wait(empty + s, parity(n) ^ 1u, a.timeout_ns)) {
+          fail = 1;
+          break;
+        }
+        tc::bar_expect_tx(full + s, C::kStage);
+        tc::tma_load_2d(sm + s * C::kStage, &maps.w, (k0 + n) * kGK, m0, full + s);
+      }
+      tc::tma_load_2d(sm + s * C::kStage + kGM * kGK, &maps.q, (k0 + n) * kGK, t0, full + s);
+    }
+#pragma unroll 1
+    for (int q = n > kSplitStages ? n - kSplitStages : 0; fail && q < n; ++q)  // copies under way
+      tc::bar_wait(full + q % kSplitStages, parity(q), a.timeout_ns);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = instr_desc_i8(BN);
+#pragma unroll 1
+    for (int n = 0; n < k1 - k0; ++n) {
+      const int s = n % kSplitStages;
+      if (!tc::bar_wait(full + s, parity(n), a.timeout_ns)) {
+        fail = 1;
+        for (int q = n; q < k1 - k0 && q < n + kSplitStages; ++q)  // copies under way
+          tc::bar_wait(full + q % kSplitStages, parity(q), a.timeout_ns);
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint64_t da = tc::smem_desc(tc::sa(sm + s * C::kStage)), db = tc::smem_desc(tc::sa(sm + s * C::kStage + kGM * kGK));
+#pragma unroll
+      for (int i = 0; i < kGK / 32; ++i) mma_i8(tmem, da + 2 * i, db + 2 * i, idesc, n > 0 || i > 0);
+      tc::mma_commit(empty + s);
+    }
+    tc::mma_commit(done);  // (of what was issued, where a wait ran out)
+  }
+  __syncwarp();
+  if (!tc::bar_wait(done, 0, 2 * a.timeout_ns)) fail = 1;
+  if (fail) report(a.err, 5 /* MOE_ERR_TIMEOUT */);
+  __syncwarp();
+  int* sums = reinterpret_cast<int*>(sm);  // [BN][128]; the MMAs have read their operands
+  __syncthreads();
+  if (warp >= 2) {
+    const int quad = warp & 3;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+    for (int c = 0; c < BN && t0 + c < a.lin.T; c += 32) {
+      float v[32];
+      tc::tmem_ld32(tmem + c + (static_cast<uint32_t>(quad * 32) << 16), v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sums[(c + i) * kGM + quad * 32 + lane] = __float_as_int(v[i]);
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  }
+  dependency_wait();
+  cluster_sync();
+  {
+    // a thread per (row, column): rank takes every S-th column; 192 threads: row = tid % 64 (+ 64), column = tid / 64
+    const uint32_t base = tc::sa(sums);
+#pragma unroll 1
+    for (int c = rank + S * (tid >> 6); c < BN && t0 + c < a.lin.T; c += 3 * S) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = (tid & 63) + 64 * h, n = m0 + row;
+        if (n >= a.lin.N) continue;
+        int v = 0;
+#pragma unroll 1
+        for (int p = 0; p < S; ++p) {
+          uint32_t at;
+          int x;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + (c * kGM + row) * 4), "r"(p));
+          asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+          v += x;
+        }
+        const float y = fmaf(static_cast<float>(v) * __ldg(a.lin.sx + t0 + c), __ldg(a.lin.sw + n),
+                             a.lin.bias ? __ldg(a.lin.bias + n) : 0.f);
+        const size_t o = static_cast<size_t>(t0 + c) * a.lin.N + n;
+        if (MODE == 1) {
+          static_cast<__nv_bfloat16*>(a.lin.out)[o] = __float2bfloat16_rn(y);
+        } else {
+          float* q = static_cast<float*>(a.lin.out) + o;
+          *q = MODE == 2 ? *q + y : y;
+        }
+      }
+    }
+  }
+  cluster_sync();  // nobody reads this CTA's sums any more
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(BN));
   }
 }
 

@@ -20,15 +20,36 @@ int64_t row_bytes(int32_t n) { return (static_cast<int64_t>(n) + 15) / 16 * 16; 
 
 bool dim_ok(int32_t n) { return n >= 1 && n <= MOE_I8_MAX_IN; }
 
-template <int NT>
-void launch_rows(const l8::LinArgs& a, cudaStream_t st) {
-  const int tiles = (a.N + 15) / 16, steps = (a.K16 + 3) / 4;
-  // split K over warps until there are 16 warps a multiprocessor, with four 64-byte steps a warp at least
+// Launch with leave to start while the kernel before it in the stream runs, if that one allows it (the quantiser
+// does): what the kernels here read of its results they read after waiting for it.
+template <class... P, class... A>
+moe_status launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&c, kern, static_cast<P>(args)...) == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
+template <int R, int NT>
+moe_status launch_rows(const l8::LinArgs& a, int nsm, cudaStream_t st) {
+  const int groups = (a.N + R - 1) / R;
+  // split K over warps until there are 32 warps a multiprocessor, with a chunk for every lane at least
   int kw = 1;
-  while (kw < l8::kRowWarps && tiles * kw < 148 * 16 && steps >= 8 * kw) kw *= 2;
+  while (kw < l8::kRowWarps && groups * kw < nsm * 32 && a.K16 >= 64 * kw) kw *= 2;
   const int per = l8::kRowWarps / kw;
-  dim3 grid((tiles + per - 1) / per, (a.T + NT * 8 - 1) / (NT * 8));
-  l8::rows_kernel<NT><<<grid, 32 * l8::kRowWarps, 0, st>>>(a, kw);
+  return launch_after(l8::rows_kernel<R, NT>, dim3((groups + per - 1) / per), 32 * l8::kRowWarps, 0, 1, st, a, kw);
 }
 
 constexpr int kMaxDev = 64;
@@ -85,23 +106,52 @@ moe_status launch_gemm_mode(const l8::GemmMaps& maps, const l8::GemmArgs& a, int
     allowed[dev].store(true, std::memory_order_relaxed);
   }
   const int tiles = a.m_tiles * a.n_tiles;
-  kern<<<tiles < nsm ? tiles : nsm, l8::kGThreads, l8::GemmCfg<BN>::kSmem, st>>>(maps, a);
-  return launched();
+  return launch_after(kern, dim3(tiles < nsm ? tiles : nsm), l8::kGThreads, l8::GemmCfg<BN>::kSmem, 1, st, maps, a);
+}
+
+template <int BN, int MODE>
+moe_status launch_split_mode(const l8::GemmMaps& maps, const l8::GemmArgs& a, int S, int dev, cudaStream_t st) {
+  auto kern = l8::split_kernel<BN, MODE>;
+  static std::atomic<bool> allowed[kMaxDev];
+  if (!allowed[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, l8::SplitCfg<BN>::kSmem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    allowed[dev].store(true, std::memory_order_relaxed);
+  }
+  return launch_after(kern, dim3(a.m_tiles * S, a.n_tiles), l8::kSplitThreads, l8::SplitCfg<BN>::kSmem, S, st, maps, a, S);
+}
+
+template <int BN>
+bool make_args(l8::GemmMaps* maps, l8::GemmArgs* a, const l8::LinArgs& lin, int in_dim, int* err) {
+  a->lin = lin;
+  a->KT = (in_dim + l8::kGK - 1) / l8::kGK;
+  a->m_tiles = (lin.N + l8::kGM - 1) / l8::kGM;
+  a->n_tiles = (lin.T + BN - 1) / BN;
+  a->err = err;
+  a->timeout_ns = 2000000000LL;
+  return codes_map(&maps->w, lin.W, in_dim, lin.N, lin.ldw, l8::kGM) &&
+         codes_map(&maps->q, lin.q, in_dim, lin.T, lin.ldq, BN);
+}
+
+template <int BN>
+moe_status launch_split(const l8::LinArgs& lin, int in_dim, int* err, int nsm, int dev, cudaStream_t st) {
+  l8::GemmMaps maps;
+  l8::GemmArgs a{};
+  if (!make_args<BN>(&maps, &a, lin, in_dim, err)) return MOE_ERR_CUDA;
+  int S = 1;
+  while (S < 8 && a.m_tiles * a.n_tiles * S * 2 <= nsm && a.KT >= 2 * S) S *= 2;
+  switch (lin.out_mode) {
+    case 0: return launch_split_mode<BN, 0>(maps, a, S, dev, st);
+    case 1: return launch_split_mode<BN, 1>(maps, a, S, dev, st);
+    default: return launch_split_mode<BN, 2>(maps, a, S, dev, st);
+  }
 }
 
 template <int BN>
 moe_status launch_gemm(const l8::LinArgs& lin, int in_dim, int* err, int nsm, int dev, cudaStream_t st) {
   l8::GemmMaps maps;
-  if (!codes_map(&maps.w, lin.W, in_dim, lin.N, lin.ldw, l8::kGM) ||
-      !codes_map(&maps.q, lin.q, in_dim, lin.T, lin.ldq, BN))
-    return MOE_ERR_CUDA;
   l8::GemmArgs a{};
-  a.lin = lin;
-  a.KT = (in_dim + l8::kGK - 1) / l8::kGK;
-  a.m_tiles = (lin.N + l8::kGM - 1) / l8::kGM;
-  a.n_tiles = (lin.T + BN - 1) / BN;
-  a.err = err;
-  a.timeout_ns = 2000000000LL;
+  if (!make_args<BN>(&maps, &a, lin, in_dim, err)) return MOE_ERR_CUDA;
   switch (lin.out_mode) {
     case 0: return launch_gemm_mode<BN, 0>(maps, a, nsm, dev, st);
     case 1: return launch_gemm_mode<BN, 1>(maps, a, nsm, dev, st);
@@ -124,10 +174,12 @@ moe_status moe_quant_i8(const void* x, int32_t x_type, int32_t T, int32_t H, flo
   if (!x || !q || !scale || !aligned16(q)) return MOE_ERR_INVALID_ARG;
   l8::QuantArgs a{x, T, H, eps, q, ldq, scale};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // whole 8-value pieces: rows that begin on 16 bytes (and their codes on 8)
+  const bool vec = H % 8 == 0 && aligned16(x);
   if (x_type == 1)
-    l8::quant_kernel<true><<<T, l8::kQThreads, 0, st>>>(a);
+    (vec ? l8::quant_kernel<true, true> : l8::quant_kernel<true, false>)<<<T, l8::kQThreads, 0, st>>>(a);
   else
-    l8::quant_kernel<false><<<T, l8::kQThreads, 0, st>>>(a);
+    (vec ? l8::quant_kernel<false, true> : l8::quant_kernel<false, false>)<<<T, l8::kQThreads, 0, st>>>(a);
   return launched();
 }
 
@@ -155,30 +207,24 @@ moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, con
   a.out = out;
   a.out_mode = out_mode;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (T <= 8)
-    launch_rows<1>(a, st);
-  else if (T <= 16)
-    launch_rows<2>(a, st);
-  else if (T <= 32)
-    launch_rows<4>(a, st);
-  else if (T <= 64)
-    launch_rows<8>(a, st);
-  else {
-    int dev = 0;
-    const int nsm = multiprocessors(&dev);
-    if (nsm < 1) return MOE_ERR_CUDA;
-    // the token tile whose waves of tiles take the least time: a tile costs its columns, and 16 more for its turn
-    auto cost = [&](int bn) {
-      const long long tiles = static_cast<long long>((a.N + l8::kGM - 1) / l8::kGM) * ((T + bn - 1) / bn);
-      return (tiles + nsm - 1) / nsm * (bn + 16);
-    };
-    const long long c256 = cost(256), c192 = cost(192), c128 = cost(128), c64 = cost(64);
-    if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_gemm<256>(a, W->in_dim, err_word, nsm, dev, st);
-    if (c192 <= c128 && c192 <= c64) return launch_gemm<192>(a, W->in_dim, err_word, nsm, dev, st);
-    if (c128 <= c64) return launch_gemm<128>(a, W->in_dim, err_word, nsm, dev, st);
-    return launch_gemm<64>(a, W->in_dim, err_word, nsm, dev, st);
-  }
-  return launched();
+  int dev = 0;
+  const int nsm = multiprocessors(&dev), in = W->in_dim;
+  if (nsm < 1) return MOE_ERR_CUDA;
+  if (T == 1) return launch_rows<4, 1>(a, nsm, st);
+  if (T == 2) return launch_rows<4, 2>(a, nsm, st);
+  if (T <= 4) return launch_rows<4, 4>(a, nsm, st);
+  if (T <= 8) return launch_rows<2, 8>(a, nsm, st);
+  const long long m = (a.N + l8::kGM - 1) / l8::kGM;
+  auto tiles = [&](int bn) { return m * ((T + bn - 1) / bn); };
+  if (tiles(32) <= nsm || (T <= 32 && tiles(32) <= 4 * nsm)) return launch_split<32>(a, in, err_word, nsm, dev, st);
+  if (tiles(64) <= nsm) return launch_split<64>(a, in, err_word, nsm, dev, st);
+  // the token tile whose waves of tiles take the least time: a tile costs its columns, and 16 more for its turn
+  auto cost = [&](int bn) { return (tiles(bn) + nsm - 1) / nsm * (bn + 16); };
+  const long long c256 = cost(256), c192 = cost(192), c128 = cost(128), c64 = cost(64);
+  if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_gemm<256>(a, in, err_word, nsm, dev, st);
+  if (c192 <= c128 && c192 <= c64) return launch_gemm<192>(a, in, err_word, nsm, dev, st);
+  if (c128 <= c64) return launch_gemm<128>(a, in, err_word, nsm, dev, st);
+  return launch_gemm<64>(a, in, err_word, nsm, dev, st);
 }
 
 }  // extern "C"

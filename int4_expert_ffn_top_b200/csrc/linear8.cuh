@@ -240,24 +240,30 @@ __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, i
 }
 
 // ----------------------------------------------------------------------------- many tokens: tcgen05 kind::i8
-// D[n][t] = sum_k W[n][k] q[t][k]: 128 weight rows are the MMA's M side, BN tokens its N side, 32-bit integer
-// accumulators in tensor memory.  Persistent and warp-specialised: warp 0 brings 128-byte K slices of both operands by
-// TMA (128-byte swizzle, kStages of them, zero-filled past the matrices' edges), warp 1 issues the MMAs (four k32 steps a
-// slice), eight epilogue warps (TMEM lane quadrant = warp % 4, two warps per quadrant splitting the columns) drain one
-// accumulator while the next tile's MMAs fill the other.  A lane is a weight row and a column a token, so the 32 lanes
-// of a store write 32 neighbouring outputs of one token.
+// D[n][t] = sum_k W[n][k] q[t][k]: weight rows are the MMA's M side, tokens its N side, 32-bit integer accumulators in
+// tensor memory.  A pair of CTAs (cta_group::2) works on 256 weight rows x BN tokens: each holds 128 of the rows and
+// half of the tokens in its shared memory and the tensor cores of both read both halves of the tokens.  An 8-bit tile of
+// one CTA (128 x 256) asks its shared memory for 192 bytes a cycle (operands in by TMA, out to the MMA), more than the
+// 128 it has; the pair's share is 128: 8,192 x 4,096 -> 4,096 takes xx us against 98.7 us.
+// Persistent and warp-specialised: warp 0 brings 128-byte K slices of both operands by TMA (128-byte swizzle, zero-filled
+// past the matrices' edges), both CTAs' slices counted by the first CTA's barrier; warp 1 of the first CTA issues the
+// MMAs (four k32 steps a slice) and its commits free the stages of both; eight epilogue warps (TMEM lane quadrant =
+// warp % 4, two warps per quadrant splitting the columns) drain one accumulator while the next tile's MMAs fill the
+// other.  A lane is a weight row and a column a token, so the 32 lanes of a store write 32 neighbouring outputs of one
+// token.
 // Every wait is bounded: a role whose wait runs out stops and records MOE_ERR_TIMEOUT; copies and MMAs under way are
 // waited for (bounded) before the CTA leaves.
 constexpr int kGM = 128, kGK = 128;
 constexpr int kGEpiWarps = 8, kGThreads = 64 + 32 * kGEpiWarps;
 
 template <int BN>
-struct GemmCfg {
-  static constexpr int kStage = (kGM + BN) * kGK;
-  static constexpr int kStages = BN >= 256 ? 4 : (BN >= 192 ? 5 : (BN >= 128 ? 6 : 8));
+struct GemmCfg {  // per CTA
+  static constexpr int kStage = (kGM + BN / 2) * kGK;
+  static constexpr int kStages = BN >= 256 ? 6 : (BN >= 192 ? 6 : 8);
   static constexpr int kSxBytes = 2 * BN * 4;
   static constexpr int kSmem = 1024 + kStages * kStage + kSxBytes + 256;
-  static constexpr uint32_t kCols = 2 * BN <= 64 ? 64 : (2 * BN <= 128 ? 128 : (2 * BN <= 256 ? 256 : 512));
+  static constexpr uint32_t kCols = 2 * BN <= 128 ? 128 : (2 * BN <= 256 ? 256 : 512);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct GemmMaps {
@@ -271,15 +277,51 @@ struct GemmArgs {
   long long timeout_ns;
 };
 
-// Instruction descriptor, kind::i8: signed 8-bit A and B (K-major), 32-bit integer accumulator, M = 128, N = n.
-MOE_DEV uint32_t instr_desc_i8(int n) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptor, kind::i8: signed 8-bit A and B (K-major), 32-bit integer accumulator.
+MOE_DEV uint32_t instr_desc_i8(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+template <int CTAS>
 MOE_DEV void mma_i8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CTAS == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+            tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+            tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// Arrive on the barrier at this offset in both CTAs of the pair when the MMAs issued so far are done.
+MOE_DEV void commit_pair(uint64_t* b) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(tc::sa(b)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Address of CTA `rank`'s counterpart of a shared-memory address of this CTA.
+MOE_DEV uint32_t peer_addr(const void* p, int rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::sa(p)), "r"(rank));
+  return at;
+}
+
+// 2-D TMA load into this CTA's shared memory, counted by a barrier of either CTA of the pair (cluster address).
+MOE_DEV void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(tc::sa(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // OR of v over the 256 epilogue threads (named barrier 1).
@@ -295,18 +337,19 @@ MOE_DEV bool epi_any(bool v) {
 }
 
 template <int BN, int MODE>
-__global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constant__ GemmMaps maps,
-                                                            const __grid_constant__ GemmArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
+    gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs a) {
   using C = GemmCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* sxs = reinterpret_cast<float*>(sm + C::kStages * C::kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kStages * C::kStage + C::kSxBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kStages * C::kStage + C::kSxBytes);  // the first CTA's count both
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
-  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* acc_empty = acc_full + 2;  // the first CTA's count both CTAs' epilogue warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = a.m_tiles * a.n_tiles;
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -315,17 +358,18 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
     }
     for (int s = 0; s < 2; ++s) {
       tc::bar_init(acc_full + s, 1);
-      tc::bar_init(acc_empty + s, kGEpiWarps);
+      tc::bar_init(acc_empty + s, 2 * kGEpiWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::sa(tmem_slot)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::sa(tmem_slot)),
                  "r"(C::kCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
   int fail = 0;
@@ -336,8 +380,8 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
       dependency_wait();
       int n = 0;
 #pragma unroll 1
-      for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x) {
-        const int m0 = (t % a.m_tiles) * kGM, t0 = (t / a.m_tiles) * BN;
+      for (int t = pair; t < tiles && !fail; t += pairs) {
+        const int m0 = (t % a.m_tiles) * 2 * kGM + rank * kGM, t0 = (t / a.m_tiles) * BN + rank * (BN / 2);
 #pragma unroll 1
         for (int k = 0; k < a.KT; ++k, ++n) {
           const int s = n % C::kStages;
@@ -345,21 +389,23 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
             fail = 1;
             break;
           }
-          tc::bar_expect_tx(full + s, C::kStage);
-          tc::tma_load_2d(sm + s * C::kStage, &maps.w, k * kGK, m0, full + s);
-          tc::tma_load_2d(sm + s * C::kStage + kGM * kGK, &maps.q, k * kGK, t0, full + s);
+          if (rank == 0) tc::bar_expect_tx(full + s, 2 * C::kStage);
+          const uint32_t bar = peer_addr(full + s, 0);
+          tma_load_pair(sm + s * C::kStage, &maps.w, k * kGK, m0, bar);
+          tma_load_pair(sm + s * C::kStage + kGM * kGK, &maps.q, k * kGK, t0, bar);
         }
       }
+      // copies under way: where the stages were used up they have landed (the last ones are waited for by the epilogue)
 #pragma unroll 1
-      for (int q = n > C::kStages ? n - C::kStages : 0; fail && q < n; ++q)  // copies under way
-        tc::bar_wait(full + q % C::kStages, parity(q, C::kStages), a.timeout_ns);
+      for (int q = n > C::kStages ? n - C::kStages : 0; fail && q < n; ++q)
+        tc::bar_wait(empty + q % C::kStages, parity(q, C::kStages), a.timeout_ns);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = instr_desc_i8(BN);
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = instr_desc_i8(2 * kGM, BN);
       int n = 0, it = 0;
 #pragma unroll 1
-      for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x, ++it) {
+      for (int t = pair; t < tiles && !fail; t += pairs, ++it) {
         const int ab = it & 1;
         if (!tc::bar_wait(acc_empty + ab, parity(it, 2) ^ 1u, a.timeout_ns)) {
           fail = 1;
@@ -377,23 +423,25 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint64_t da = tc::smem_desc(tc::sa(sm + s * C::kStage)), db = tc::smem_desc(tc::sa(sm + s * C::kStage + kGM * kGK));
 #pragma unroll
-          for (int i = 0; i < kGK / 32; ++i) mma_i8(d, da + 2 * i, db + 2 * i, idesc, k > 0 || i > 0);
-          tc::mma_commit(empty + s);
+          for (int i = 0; i < kGK / 32; ++i) mma_i8<2>(d, da + 2 * i, db + 2 * i, idesc, k > 0 || i > 0);
+          commit_pair(empty + s);
         }
-        if (!fail) tc::mma_commit(acc_full + ab);
+        if (!fail) commit_pair(acc_full + ab);
       }
-      if (fail && n > 0) {  // MMAs under way
-        const int q = n - 1;
-        tc::bar_wait(empty + q % C::kStages, parity(q, C::kStages), a.timeout_ns);
+      if (fail) {  // copies and MMAs under way
+#pragma unroll 1
+        for (int q = n; q < n + C::kStages; ++q) tc::bar_wait(full + q % C::kStages, parity(q, C::kStages), a.timeout_ns / 8);
+        if (n > 0) tc::bar_wait(empty + (n - 1) % C::kStages, parity(n - 1, C::kStages), a.timeout_ns);
       }
     }
   } else {
     const int ew = warp - 2, quad = warp & 3, half = ew >> 2, et = tid - 64;
+    const uint32_t release[2] = {peer_addr(acc_empty, 0), peer_addr(acc_empty + 1, 0)};
     dependency_wait();
     int it = 0;
 #pragma unroll 1
-    for (int t = blockIdx.x; t < tiles && !fail; t += gridDim.x, ++it) {
-      const int ab = it & 1, m0 = (t % a.m_tiles) * kGM, t0 = (t / a.m_tiles) * BN;
+    for (int t = pair; t < tiles && !fail; t += pairs, ++it) {
+      const int ab = it & 1, m0 = (t % a.m_tiles) * 2 * kGM + rank * kGM, t0 = (t / a.m_tiles) * BN;
       const int n = m0 + quad * 32 + lane;
       const bool row = n < a.lin.N;
       const float sw = row ? __ldg(a.lin.sw + n) : 0.f, bias = row && a.lin.bias ? __ldg(a.lin.bias + n) : 0.f;
@@ -406,15 +454,17 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      auto let_go = [&]() {  // this warp has read its part of the accumulator
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(release[ab]) : "memory");
+      };
 #pragma unroll 1
       for (int c = half * 32; c < BN && t0 + c < a.lin.T; c += 64) {
         float v[32];
         tc::tmem_ld32(tmem + ab * BN + c + (static_cast<uint32_t>(quad * 32) << 16), v);
-        if (c + 64 >= BN || t0 + c + 64 >= a.lin.T) {  // this warp's last read of the accumulator
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(acc_empty + ab);
-        }
+        if (c + 64 >= BN || t0 + c + 64 >= a.lin.T) let_go();
         const size_t base = static_cast<size_t>(t0 + c) * a.lin.N + n;
         const int cols = min(32, a.lin.T - t0 - c);
         if (row) {
@@ -433,17 +483,15 @@ __global__ void __launch_bounds__(kGThreads, 1) gemm_kernel(const __grid_constan
           }
         }
       }
-      if (!(half * 32 < BN && t0 + half * 32 < a.lin.T)) {  // nothing to read for this warp
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(acc_empty + ab);
-      }
+      if (!(half * 32 < BN && t0 + half * 32 < a.lin.T)) let_go();  // nothing to read for this warp
     }
   }
   if (fail) report(a.err, 5 /* MOE_ERR_TIMEOUT */);
   __syncthreads();
+  cluster_sync();  // neither CTA's memory or barriers are in use by the other
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
   }
 }
 
@@ -460,10 +508,6 @@ struct SplitCfg {
   static constexpr int kSmem = 1024 + kSplitStages * kStage + 256;
   static_assert(kSplitStages * kStage >= BN * kGM * 4, "the sums fit where the operands were");
 };
-
-MOE_DEV void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
 
 template <int BN, int MODE>
 __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_constant__ GemmMaps maps,
@@ -523,7 +567,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     for (int q = n > kSplitStages ? n - kSplitStages : 0; fail && q < n; ++q)  // copies under way
       tc::bar_wait(full + q % kSplitStages, parity(q), a.timeout_ns);
   } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = instr_desc_i8(BN);
+    const uint32_t idesc = instr_desc_i8(kGM, BN);
 #pragma unroll 1
     for (int n = 0; n < k1 - k0; ++n) {
       const int s = n % kSplitStages;
@@ -536,7 +580,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint64_t da = tc::smem_desc(tc::sa(sm + s * C::kStage)), db = tc::smem_desc(tc::sa(sm + s * C::kStage + kGM * kGK));
 #pragma unroll
-      for (int i = 0; i < kGK / 32; ++i) mma_i8(tmem, da + 2 * i, db + 2 * i, idesc, n > 0 || i > 0);
+      for (int i = 0; i < kGK / 32; ++i) mma_i8<1>(tmem, da + 2 * i, db + 2 * i, idesc, n > 0 || i > 0);
       tc::mma_commit(empty + s);
     }
     tc::mma_commit(done);  // (of what was issued, where a wait ran out)
@@ -563,22 +607,23 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
   cluster_sync();
   {
     // a thread per (row, column): rank takes every S-th column; 192 threads: row = tid % 64 (+ 64), column = tid / 64
-    const uint32_t base = tc::sa(sums);
 #pragma unroll 1
     for (int c = rank + S * (tid >> 6); c < BN && t0 + c < a.lin.T; c += 3 * S) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = (tid & 63) + 64 * h, n = m0 + row;
         if (n >= a.lin.N) continue;
-        int v = 0;
-#pragma unroll 1
-        for (int p = 0; p < S; ++p) {
-          uint32_t at;
-          int x;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + (c * kGM + row) * 4), "r"(p));
-          asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
-          v += x;
+        int x[8], v = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          x[p] = 0;
+          if (p < S) {
+            const uint32_t at = peer_addr(sums + c * kGM + row, p);
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x[p]) : "r"(at) : "memory");
+          }
         }
+#pragma unroll
+        for (int p = 0; p < 8; ++p) v += x[p];
         const float y = fmaf(static_cast<float>(v) * __ldg(a.lin.sx + t0 + c), __ldg(a.lin.sw + n),
                              a.lin.bias ? __ldg(a.lin.bias + n) : 0.f);
         const size_t o = static_cast<size_t>(t0 + c) * a.lin.N + n;

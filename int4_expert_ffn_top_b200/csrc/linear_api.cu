@@ -106,7 +106,8 @@ moe_status launch_gemm_mode(const l8::GemmMaps& maps, const l8::GemmArgs& a, int
     allowed[dev].store(true, std::memory_order_relaxed);
   }
   const int tiles = a.m_tiles * a.n_tiles;
-  return launch_after(kern, dim3(tiles < nsm ? tiles : nsm), l8::kGThreads, l8::GemmCfg<BN>::kSmem, 1, st, maps, a);
+  const int pairs = tiles < nsm / 2 ? tiles : nsm / 2;
+  return launch_after(kern, dim3(2 * pairs), l8::kGThreads, l8::GemmCfg<BN>::kSmem, 1, st, maps, a);
 }
 
 template <int BN, int MODE>
@@ -121,23 +122,23 @@ moe_status launch_split_mode(const l8::GemmMaps& maps, const l8::GemmArgs& a, in
   return launch_after(kern, dim3(a.m_tiles * S, a.n_tiles), l8::kSplitThreads, l8::SplitCfg<BN>::kSmem, S, st, maps, a, S);
 }
 
-template <int BN>
-bool make_args(l8::GemmMaps* maps, l8::GemmArgs* a, const l8::LinArgs& lin, int in_dim, int* err) {
+// m_rows, box: weight rows of a tile, tokens of one copy
+bool make_args(l8::GemmMaps* maps, l8::GemmArgs* a, const l8::LinArgs& lin, int in_dim, int m_rows, int bn, int box, int* err) {
   a->lin = lin;
   a->KT = (in_dim + l8::kGK - 1) / l8::kGK;
-  a->m_tiles = (lin.N + l8::kGM - 1) / l8::kGM;
-  a->n_tiles = (lin.T + BN - 1) / BN;
+  a->m_tiles = (lin.N + m_rows - 1) / m_rows;
+  a->n_tiles = (lin.T + bn - 1) / bn;
   a->err = err;
   a->timeout_ns = 2000000000LL;
   return codes_map(&maps->w, lin.W, in_dim, lin.N, lin.ldw, l8::kGM) &&
-         codes_map(&maps->q, lin.q, in_dim, lin.T, lin.ldq, BN);
+         codes_map(&maps->q, lin.q, in_dim, lin.T, lin.ldq, box);
 }
 
 template <int BN>
 moe_status launch_split(const l8::LinArgs& lin, int in_dim, int* err, int nsm, int dev, cudaStream_t st) {
   l8::GemmMaps maps;
   l8::GemmArgs a{};
-  if (!make_args<BN>(&maps, &a, lin, in_dim, err)) return MOE_ERR_CUDA;
+  if (!make_args(&maps, &a, lin, in_dim, l8::kGM, BN, BN, err)) return MOE_ERR_CUDA;
   int S = 1;
   while (S < 8 && a.m_tiles * a.n_tiles * S * 2 <= nsm && a.KT >= 2 * S) S *= 2;
   switch (lin.out_mode) {
@@ -151,7 +152,7 @@ template <int BN>
 moe_status launch_gemm(const l8::LinArgs& lin, int in_dim, int* err, int nsm, int dev, cudaStream_t st) {
   l8::GemmMaps maps;
   l8::GemmArgs a{};
-  if (!make_args<BN>(&maps, &a, lin, in_dim, err)) return MOE_ERR_CUDA;
+  if (!make_args(&maps, &a, lin, in_dim, 2 * l8::kGM, BN, BN / 2, err)) return MOE_ERR_CUDA;
   switch (lin.out_mode) {
     case 0: return launch_gemm_mode<BN, 0>(maps, a, nsm, dev, st);
     case 1: return launch_gemm_mode<BN, 1>(maps, a, nsm, dev, st);
@@ -214,12 +215,12 @@ moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, con
   if (T == 2) return launch_rows<4, 2>(a, nsm, st);
   if (T <= 4) return launch_rows<4, 4>(a, nsm, st);
   if (T <= 8) return launch_rows<2, 8>(a, nsm, st);
-  const long long m = (a.N + l8::kGM - 1) / l8::kGM;
-  auto tiles = [&](int bn) { return m * ((T + bn - 1) / bn); };
-  if (tiles(32) <= nsm || (T <= 32 && tiles(32) <= 4 * nsm)) return launch_split<32>(a, in, err_word, nsm, dev, st);
-  if (tiles(64) <= nsm) return launch_split<64>(a, in, err_word, nsm, dev, st);
+  const long long m = (a.N + l8::kGM - 1) / l8::kGM, m2 = (m + 1) / 2;
+  auto tiles = [&](long long rows, int bn) { return rows * ((T + bn - 1) / bn); };
+  if (tiles(m, 32) <= nsm || (T <= 32 && tiles(m, 32) <= 4 * nsm)) return launch_split<32>(a, in, err_word, nsm, dev, st);
+  if (tiles(m, 64) <= nsm) return launch_split<64>(a, in, err_word, nsm, dev, st);
   // the token tile whose waves of tiles take the least time: a tile costs its columns, and 16 more for its turn
-  auto cost = [&](int bn) { return (tiles(bn) + nsm - 1) / nsm * (bn + 16); };
+  auto cost = [&](int bn) { return (tiles(m2, bn) + nsm / 2 - 1) / (nsm / 2) * (bn + 16); };
   const long long c256 = cost(256), c192 = cost(192), c128 = cost(128), c64 = cost(64);
   if (c256 <= c192 && c256 <= c128 && c256 <= c64) return launch_gemm<256>(a, in, err_word, nsm, dev, st);
   if (c192 <= c128 && c192 <= c64) return launch_gemm<192>(a, in, err_word, nsm, dev, st);

@@ -76,7 +76,8 @@ def check_linear(N, K, T, mode, bias=True, pad=0, seed=0):
 
 # ----------------------------------------------------------------------------- quantiser
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("T,H", [(1, 1), (3, 17), (5, 2048), (2, 1000), (7, 255), (1, 65536), (300, 4096), (2, 9999)])
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 17), (5, 2048), (2, 1000), (7, 255), (1, 65536), (300, 4096), (2, 9999),
+                                 (1184, 2048), (1190, 264), (1185, 257)])
 def test_codes_are_the_correctly_rounded_quotients(cuda_ok, T, H, dtype):
     g = torch.Generator(device=DEV).manual_seed(T * H)
     x = (torch.randn((T, H), device=DEV, generator=g) * torch.rand((T, 1), device=DEV, generator=g).add(0.1)).to(dtype)

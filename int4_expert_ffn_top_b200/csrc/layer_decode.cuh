@@ -41,7 +41,8 @@ constexpr int kSlotBlock = 4;  // down: slots per MMA (hi and lo columns)
 constexpr int kMaxEls = kMaxSlots + kMaxT / kSlotBlock;
 constexpr int kMaxSharedPairs = 16;  // pairs of the shared expert a CTA takes
 constexpr int kHeaderBytes = 256;
-constexpr int kUnitRow = 160, kUnitBytes = 16 * kUnitRow, kBuf = 2;  // see issue_unit
+constexpr int kUnitBytes = 16 * 128, kSetsBytes = 1024;  // see UnitPlan
+constexpr int kWarpRing = 2 * kUnitBytes + kSetsBytes;
 
 enum Bar { B_IMAGE = 0, B_LOGITS = 1, B_EXGU = 2, B_HIDDEN = 3, B_EXDOWN = 4, kBars = 5 };
 
@@ -372,49 +373,60 @@ __device__ __noinline__ void build_image(const Args& a, int t, int wi, int warps
 }
 
 // ----------------------------------------------------------------------------- int4 units
-// The unit of weight traffic and of work: 16 rows x 4 groups (2 where a row has only 2), brought by one warp into its
-// own buffers with cp.async (128 code bytes a row, then its 4 scales and 4 biases; row stride 160 bytes, 32 past a
-// multiple of 128, so that the 8-byte fragment reads of 4 rows fall on different banks) and used by that warp alone:
-// no barrier is needed between copy and use, and each of 24 warps has kBuf units of 2.3 KB, one in use and the rest in flight.
+// The unit of weight traffic and of work: the codes of 16 rows x 4 groups (2 where a row has only 2), brought by one
+// warp into its own buffers with cp.async and used by that warp alone: no barrier is needed between copy and use, and
+// each of 24 warps has two units of 2 KB, one in use and one in flight (a third takes L1 away from the token images:
+// 62 us against 57 for 16 tokens of the 35B shape).  16-byte chunk c of row m lies at place c ^ 2 (m % 4) of the row's 128 bytes, so that the 8-byte fragment reads of 4 rows fall on different banks.  The
+// scales and biases come for two units at a time (16 bytes each of a row) into sets of their own, [16 rows][scales,
+// biases].
 // Row m of a unit is record (m % 8) * step_lo + (m / 8) * step_hi: gate rows over up rows for gate/up (2, 1), rows in
 // order for down (1, 8).
 struct UnitPlan {  // a lane's places: bytes from the unit's first record (its chunk of row lane/8; its scales)
   uint32_t c0, c4, c8, c12, s;
-  uint32_t dst, dst_s;
-  bool on, four;
+  int piece;  // bytes of scales (as of biases) of a row in a set, 16 or 8 places apart
+  bool on;
+  MOE_DEV int half() const { return piece == 16 ? 16 : 8; }
+  MOE_DEV int set_bytes() const { return 32 * half(); }
   MOE_DEV void make(int rec, int G, int step_lo, int step_hi) {
     const int lane = threadIdx.x & 31, q = lane >> 3, ch = lane & 7, m = lane >> 1;
-    four = G >= 4;
-    on = ch < (four ? 8 : 2 * G);
+    on = ch < (G >= 4 ? 8 : 2 * G);
     c0 = q * step_lo * rec + 16 * ch;
     c4 = c0 + 4 * step_lo * rec;
     c8 = c0 + step_hi * rec;
     c12 = c4 + step_hi * rec;
+    piece = G >= 8 ? 16 : 2 * G;
     s = ((m & 7) * step_lo + (m >> 3) * step_hi) * rec + G * 32 + 2 * G * (lane & 1);
-    dst = q * kUnitRow + 16 * ch;
-    dst_s = m * kUnitRow + 128 + 8 * (lane & 1);
   }
 };
 
-// Copy a unit: lo and hi rows of each half exist.  base: the first record plus 128 bytes a unit; sbase: plus 8 bytes a
-// unit.
-MOE_DEV void issue_unit(uint32_t buf, const UnitPlan& p, const uint8_t* base, const uint8_t* sbase, int lo, int hi) {
-  const int lane = threadIdx.x & 31, q = lane >> 3, m = lane >> 1;
+// The codes of unit u of the records at base; lo and hi rows of each half exist.
+MOE_DEV void issue_codes(uint32_t buf, const UnitPlan& p, const uint8_t* base, int u, int lo, int hi) {
+  const int lane = threadIdx.x & 31, q = lane >> 3;
   auto cp16 = [](uint32_t d, const uint8_t* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
   };
-  const uint32_t d = buf + p.dst;
+  const uint32_t d = buf + q * 128 + 16 * ((lane & 7) ^ 2 * q);  // q + 4, + 8, + 12: the same places
+  base += 128 * u;
   if (p.on) {
     if (q < lo) cp16(d, base + p.c0);
-    if (q + 4 < lo) cp16(d + 4 * kUnitRow, base + p.c4);
-    if (q < hi) cp16(d + 8 * kUnitRow, base + p.c8);
-    if (q + 4 < hi) cp16(d + 12 * kUnitRow, base + p.c12);
+    if (q + 4 < lo) cp16(d + 4 * 128, base + p.c4);
+    if (q < hi) cp16(d + 8 * 128, base + p.c8);
+    if (q + 4 < hi) cp16(d + 12 * 128, base + p.c12);
   }
+}
+
+// The scales and biases of units u and u ^ 1.
+MOE_DEV void issue_scales(uint32_t set, const UnitPlan& p, const uint8_t* base, int u, int lo, int hi) {
+  const int lane = threadIdx.x & 31, m = lane >> 1;
+  const uint32_t d = set + p.half() * lane;
+  base += p.s + 16 * (u >> 1);
   if ((m & 7) < (m < 8 ? lo : hi)) {
-    if (p.four)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(buf + p.dst_s), "l"(sbase + p.s) : "memory");
+    if (p.piece == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(base) : "memory");
+    else if (p.piece == 8)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(base) : "memory");
     else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(buf + p.dst_s), "l"(sbase + p.s) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(base) : "memory");
   }
 }
 
@@ -429,27 +441,31 @@ MOE_DEV Frag load_frag(const uint8_t* col, int i) {
 
 // acc += one unit of gate/up rows times 8 columns, two groups at a time (four would take half as many warps again in
 // registers).
-MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* col, const float* ua, const float* ub, float (&acc)[4]) {
+MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* set, int half, const uint8_t* col, const float* ua, const float* ub,
+                          float (&acc)[4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const uint8_t* ra = buf + g * kUnitRow;
-  const uint8_t* rb = ra + 8 * kUnitRow;
+  // chunk 2 i + tig / 2 of row g (and g + 8)
+  const uint8_t* ra = buf + g * 128 + 8 * (tig & 1);
+  const int ch = (tig >> 1) ^ 2 * (g & 3);
   const uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
+  const uint8_t* sp = set + 2 * half * g;
+  const uint2 sa2 = *reinterpret_cast<const uint2*>(sp), ba2 = *reinterpret_cast<const uint2*>(sp + half);
+  const uint2 sb2 = *reinterpret_cast<const uint2*>(sp + 16 * half), bb2 = *reinterpret_cast<const uint2*>(sp + 17 * half);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float d[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const Frag f = load_frag(col, 2 * h + i);
-      const uint2 wa = *reinterpret_cast<const uint2*>(ra + (2 * h + i) * 32 + tig * 8);
-      const uint2 wb = *reinterpret_cast<const uint2*>(rb + (2 * h + i) * 32 + tig * 8);
+      const uint8_t* w = ra + 16 * (ch ^ (4 * h + 2 * i));
+      const uint2 wa = *reinterpret_cast<const uint2*>(w), wb = *reinterpret_cast<const uint2*>(w + 1024);
       const uint32_t wa8 = wa.x >> 8, wb8 = wb.x >> 8, va8 = wa.y >> 8, vb8 = wb.y >> 8;
       mma16_0(d[i], wa.x & lo, wb.x & lo, wa.x & hi, wb.x & hi, f.x.x, f.x.y);
       mma16(d[i], wa8 & lo, wb8 & lo, wa8 & hi, wb8 & hi, f.x.z, f.x.w);
       mma16(d[i], wa.y & lo, wb.y & lo, wa.y & hi, wb.y & hi, f.y.x, f.y.y);
       mma16(d[i], va8 & lo, vb8 & lo, va8 & hi, vb8 & hi, f.y.z, f.y.w);
     }
-    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(ra + 128 + 4 * h), b0 = *reinterpret_cast<const uint32_t*>(ra + 136 + 4 * h);
-    const uint32_t s1 = *reinterpret_cast<const uint32_t*>(rb + 128 + 4 * h), b1 = *reinterpret_cast<const uint32_t*>(rb + 136 + 4 * h);
+    const uint32_t s0 = h ? sa2.y : sa2.x, b0 = h ? ba2.y : ba2.x, s1 = h ? sb2.y : sb2.x, b1 = h ? bb2.y : bb2.x;
     const float2 u = *reinterpret_cast<const float2*>(ua + 2 * h), v = *reinterpret_cast<const float2*>(ub + 2 * h);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -463,18 +479,22 @@ MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* col, const float* u
   }
 }
 
-// acc += one unit of down rows (15 of them; row 15 sums the columns) times the 8 columns (hi and lo of 4 slots).
+// acc += one unit of down rows (15 of them; row 15 holds code 15 everywhere: 15 times the columns' sums) times the 8
+// columns (hi and lo of 4 slots).
 // Codes enter as code 2^-22 (and 16 times that).  The MMA aligns its products by their exponents, and a subnormal
 // counts with the smallest one, so two more of the mantissa's bits in use keep two more of h's 11 in the sum (u's 8 fit
 // either way): the result is off by 7e-7 of its size instead of 3e-6.
-MOE_DEV void down_unit(const uint8_t* buf, Frag f0, Frag f1, const uint8_t* col, bool whole, float (&acc)[4]) {
+MOE_DEV void down_unit(const uint8_t* buf, const uint8_t* set, int half, Frag f0, Frag f1, const uint8_t* col, bool whole,
+                       float (&acc)[4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-  const bool ones = g == 7;
-  const uint8_t* ra = buf + g * kUnitRow;
-  const uint8_t* rb = ones ? ra : ra + 8 * kUnitRow;
-  const uint32_t lo = 0x003C003Cu, hi = 0x03C003C0u, one = 0x3C003C00u, sixteen = 0x4C004C00u;
+  const uint8_t* ra = buf + g * 128 + 8 * (tig & 1);
+  const int ch = (tig >> 1) ^ 2 * (g & 3);
+  const uint32_t lo = 0x003C003Cu, hi = 0x03C003C0u;
   Frag f2 = f0, f3 = f1;
   if (whole) f2 = load_frag(col, 2), f3 = load_frag(col, 3);
+  const uint8_t *sp = set + 2 * half * g, *sq = sp + 16 * half;
+  const uint2 sa2 = *reinterpret_cast<const uint2*>(sp), ba2 = *reinterpret_cast<const uint2*>(sp + half);
+  const uint2 sb2 = *reinterpret_cast<const uint2*>(sq), bb2 = *reinterpret_cast<const uint2*>(sq + half);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h && !whole) break;  // a row of two groups
@@ -482,21 +502,20 @@ MOE_DEV void down_unit(const uint8_t* buf, Frag f0, Frag f1, const uint8_t* col,
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const Frag& f = h ? (i ? f3 : f2) : (i ? f1 : f0);
-      const uint2 wa = *reinterpret_cast<const uint2*>(ra + (2 * h + i) * 32 + tig * 8);
-      const uint2 wb = *reinterpret_cast<const uint2*>(rb + (2 * h + i) * 32 + tig * 8);
+      const uint8_t* w = ra + 16 * (ch ^ (4 * h + 2 * i));
+      const uint2 wa = *reinterpret_cast<const uint2*>(w), wb = *reinterpret_cast<const uint2*>(w + 1024);
       const uint32_t p0 = wa.x << 2, p1 = wa.x >> 6, p2 = wa.y << 2, p3 = wa.y >> 6;
       const uint32_t q0 = wb.x << 2, q1 = wb.x >> 6, q2 = wb.y << 2, q3 = wb.y >> 6;
-      mma16_0(d[i], p0 & lo, ones ? one : q0 & lo, p0 & hi, ones ? sixteen : q0 & hi, f.x.x, f.x.y);
-      mma16(d[i], p1 & lo, ones ? one : q1 & lo, p1 & hi, ones ? sixteen : q1 & hi, f.x.z, f.x.w);
-      mma16(d[i], p2 & lo, ones ? one : q2 & lo, p2 & hi, ones ? sixteen : q2 & hi, f.y.x, f.y.y);
-      mma16(d[i], p3 & lo, ones ? one : q3 & lo, p3 & hi, ones ? sixteen : q3 & hi, f.y.z, f.y.w);
+      mma16_0(d[i], p0 & lo, q0 & lo, p0 & hi, q0 & hi, f.x.x, f.x.y);
+      mma16(d[i], p1 & lo, q1 & lo, p1 & hi, q1 & hi, f.x.z, f.x.w);
+      mma16(d[i], p2 & lo, q2 & lo, p2 & hi, q2 & hi, f.y.x, f.y.y);
+      mma16(d[i], p3 & lo, q3 & lo, p3 & hi, q3 & hi, f.y.z, f.y.w);
     }
-    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(ra + 128 + 4 * h), b0 = *reinterpret_cast<const uint32_t*>(ra + 136 + 4 * h);
-    const uint32_t s1 = *reinterpret_cast<const uint32_t*>(rb + 128 + 4 * h), b1 = *reinterpret_cast<const uint32_t*>(rb + 136 + 4 * h);
+    const uint32_t s0 = h ? sa2.y : sa2.x, b0 = h ? ba2.y : ba2.x, s1 = h ? sb2.y : sb2.x, b1 = h ? bb2.y : bb2.x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float u = __shfl_sync(0xffffffffu, d[i][2], 28 + tig) * 0x1p-22f;
-      const float v = __shfl_sync(0xffffffffu, d[i][3], 28 + tig) * 0x1p-22f;
+      const float u = __shfl_sync(0xffffffffu, d[i][2], 28 + tig) * (1.f / 15.f);
+      const float v = __shfl_sync(0xffffffffu, d[i][3], 28 + tig) * (1.f / 15.f);
       const float p = i ? hi_half(s0) : lo_half(s0), q = i ? hi_half(b0) : lo_half(b0);
       const float r = i ? hi_half(s1) : lo_half(s1), t = i ? hi_half(b1) : lo_half(b1);
       acc[0] = fmaf(q, u, fmaf(p, d[i][0], acc[0]));
@@ -641,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   int* els = reinterpret_cast<int*>(sm + S.els);
   float* scratch = reinterpret_cast<float*>(sm + S.scratch);
   float* sraw = reinterpret_cast<float*>(sm + S.sraw);
-  uint8_t* ring = sm + S.ring + warp * (kBuf * kUnitBytes);
+  uint8_t* ring = sm + S.ring + warp * kWarpRing;  // codes, then sets of scales
+  uint8_t* sets = ring + 2 * kUnitBytes;
 
   // this CTA's shares: pairs of the shared expert, rows of the down projections, rows over all tokens
   const int sp0 = share(cta, a.I, a.gmul), nsp = share(cta + 1, a.I, a.gmul) - sp0, nst = (nsp + 7) / 8;
@@ -661,14 +681,17 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   }
   // --------------------------------------------------------------------------- weights that no token decides
   // The first shared tile's units: unit warp % U for token blocks warp / U, + sh_n, ...
-  const uint32_t ring32 = sa(ring);
+  const uint32_t ring32 = sa(ring), sets32 = sa(sets);
   const int sh_ways = max(1, min(nblk, kWarps >> a.logU));
   UnitPlan plan;
   plan.make(RGU, G, 2, 1);
   {
     const uint8_t* src = a.shared + static_cast<size_t>(2 * sp0) * RGU;
     const int u = warp & (U - 1), n = min(8, nsp);
-    if (nst > 0 && warp < U * sh_ways) issue_unit(ring32, plan, src + 128 * u, src + 8 * u, n, n);
+    if (nst > 0 && warp < U * sh_ways) {
+      issue_codes(ring32, plan, src, u, n, n);
+      issue_scales(sets32, plan, src, u, n, n);
+    }
     cp_commit();
   }
   const int g0 = warp * G / kWarps, g1 = (warp + 1) * G / kWarps;  // groups of the rows over all tokens: up to 3
@@ -789,14 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
       if (ti > 0) {
         const uint8_t* src = a.shared + static_cast<size_t>(2 * (sp0 + 8 * ti)) * RGU;
         const int n = min(8, nsp - 8 * ti);
-        issue_unit(ring32, plan, src + 128 * u, src + 8 * u, n, n);
+        issue_codes(ring32, plan, src, u, n, n);
+        issue_scales(sets32, plan, src, u, n, n);
         cp_commit();
       }
       cp_wait<0>();
 #pragma unroll 1
       for (int b = task >> a.logU; b < nblk; b += sh_ways) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        gate_up_unit(ring, img + static_cast<size_t>(min(8 * b + g, T - 1)) * ldu + u * 512,
+        gate_up_unit(ring, sets + (U > 1 ? 8 * (u & 1) : 0), plan.half(), img + static_cast<size_t>(min(8 * b + g, T - 1)) * ldu + u * 512,
                      us + min(8 * b + 2 * tig, T - 1) * G + 4 * u, us + min(8 * b + 2 * tig + 1, T - 1) * G + 4 * u, acc);
         *reinterpret_cast<float4*>(scratch + ((b * U + u) * 32 + lane) * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       }
@@ -920,142 +944,125 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     const int total = items << a.logU;
     auto border = [&](int w) { return static_cast<int>(static_cast<uint32_t>(total * w) / kWarps); };
     const int ub = border(warp), ue = border(warp + 1);
-    struct At {  // a place in the CTA's run of units: tile, block of slots, unit
-      int t, b, u;
-    };
-    At at{t0, 0, ub & (U - 1)};
+    // the warp's item: tile t, block of slots b, units u .. end - 1 of it here; `left` units after them
+    int t = t0, b = 0, u = ub & (U - 1), left = ue - ub;
     {
       int i = ub >> a.logU;  // item of the first unit
 #pragma unroll 1
-      while (at.t < t1) {
-        const int d = at.t >> logt, e = min(t1, (d + 1) << logt), nb = blocks(d), n = (e - at.t) * nb;
+      while (t < t1) {
+        const int d = t >> logt, e = min(t1, (d + 1) << logt), nb = blocks(d), n = (e - t) * nb;
         if (i < n) {
           const int q = nb == 1 ? i : i / nb;
-          at.t += q;
-          at.b = 8 * (i - q * nb);
+          t += q;
+          b = 8 * (i - q * nb);
           break;
         }
         i -= n;
-        at.t = e;
+        t = e;
       }
     }
-    At is = at;
-    int to_copy = ue - ub;
-    const uint8_t* ibase = nullptr;
-    auto open = [&]() { ibase = a.pool + dist[is.t >> logt] * a.stride + static_cast<size_t>(16 * (is.t & tmask)) * RGU; };
-    if (to_copy > 0) open();
-    uint32_t wr = ring32;
-    auto copy_next = [&]() {
-      if (to_copy > 0) {
-        --to_copy;
-        issue_unit(wr, plan, ibase + 128 * is.u, ibase + 8 * is.u, 8, 8);
-        if (++is.u == U) {
-          is.u = 0;
-          is.b += 8;
-          const int d = is.t >> logt;
-          if (is.b >= start[d + 1] - start[d]) {
-            is.b = 0;
-            ++is.t;
-            if (to_copy > 0) open();
-          }
-        }
-      }
-      cp_commit();
-      if ((wr += kUnitBytes) == ring32 + kBuf * kUnitBytes) wr = ring32;
+    auto records = [&](int tile) {
+      return a.pool + dist[tile >> logt] * a.stride + static_cast<size_t>(16 * (tile & tmask)) * RGU;
     };
-#pragma unroll 1
-    for (int i = 0; i < kBuf - 1; ++i) copy_next();
+    const uint8_t* base = a.pool;
+    uint32_t flip = 0;           // buffer of the unit that comes next to be used
+    uint32_t wset = sets32;      // set that comes next to be filled
+    auto copy = [&](const uint8_t* from, int unit, bool scales, uint32_t buf) {
+      issue_codes(ring32 + buf * kUnitBytes, plan, from, unit, 8, 8);
+      if (scales) {
+        issue_scales(wset, plan, from, unit, 8, 8);
+        if ((wset += plan.set_bytes()) == sets32 + kSetsBytes) wset = sets32;
+      }
+    };
+    if (left > 0) {
+      base = records(t);
+      copy(base, u, true, 0);
+    }
+    cp_commit();
 
     // the shared expert's hidden values while the first copies are under way: a pair of lanes per (token, pair)
 #pragma unroll 1
-    for (int t = kWarps - 1 - warp; t < T && nsp > 0; t += kWarps) {
+    for (int tk = kWarps - 1 - warp; tk < T && nsp > 0; tk += kWarps) {
       const int pr = min(lane >> 1, nsp - 1), up = lane & 1;
-      const float2 v = reinterpret_cast<const float2*>(sraw)[t * 16 + pr];
+      const float2 v = reinterpret_cast<const float2*>(sraw)[tk * 16 + pr];
       float x = up ? v.y : v.x;
       const uint16_t* B = up ? a.shB[1] : a.shB[0];
       if (up ? a.shA[1] != nullptr : a.shA[0] != nullptr)
-        x = fmaf(a.lora_scale, dot_r(B + static_cast<size_t>(sp0 + pr) * r, a.aux + t * (4 + 2 * r) + 4 + (up && a.shA[0] ? r : 0), r), x);
+        x = fmaf(a.lora_scale, dot_r(B + static_cast<size_t>(sp0 + pr) * r, a.aux + tk * (4 + 2 * r) + 4 + (up && a.shA[0] ? r : 0), r), x);
       __syncwarp();
       const float y = __shfl_xor_sync(0xffffffffu, x, 1);
-      if (!up && lane < 2 * nsp) store_h(a, TK + t, sp0 + pr, x, y);
+      if (!up && lane < 2 * nsp) store_h(a, TK + tk, sp0 + pr, x, y);
     }
 
-    uint8_t* rd = ring;
-    int d = 0, s0 = 0, cnt = 0;
-    const uint8_t* col = nullptr;
-    const float *ua = nullptr, *uc = nullptr;
-    auto columns = [&]() {  // of item (at.t, at.b)
-      d = at.t >> logt;
-      s0 = start[d];
-      cnt = start[d + 1] - s0;
-      const int c0 = s0 + at.b, cl = s0 + cnt - 1;
-      col = img + static_cast<size_t>(slots[min(c0 + g, cl)] >> 16) * ldu;
-      ua = us + (slots[min(c0 + 2 * tig, cl)] >> 16) * G;
-      uc = us + (slots[min(c0 + 2 * tig + 1, cl)] >> 16) * G;
-    };
+    const uint8_t* set = sets;
     float4* part = reinterpret_cast<float4*>(scratch);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    bool mine = at.u == 0;
-    auto finish = [&]() {  // hidden values of item (at.t, at.b)
-      const int j = (at.t & tmask) * 8 + g;
+    auto finish = [&]() {  // hidden values of item (t, b)
+      const int d = t >> logt, q0 = start[d] + b + 2 * tig, q1 = min(q0 + 2, start[d + 1]), j = (t & tmask) * 8 + g;
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        const int q = s0 + at.b + 2 * tig + c;
-        if (q >= s0 + cnt) break;
+      for (int q = q0; q < q1; ++q) {
         const int sl = slots[q] & 0xffff;
         const float k = ic[slots[q] >> 16] * 0x1p24f;
-        float x = (c ? acc[1] : acc[0]) * k, y = (c ? acc[3] : acc[2]) * k;
+        float x = (q > q0 ? acc[1] : acc[0]) * k, y = (q > q0 ? acc[3] : acc[2]) * k;
         if (a.exAgu) {
           const uint16_t* B = a.exBgu + (static_cast<size_t>(dist[d]) * 2 * a.I + 2 * j) * r;
-          const float* t = a.tgu + static_cast<size_t>(sl) * 2 * r;
-          x = fmaf(a.lora_scale, dot_r(B, t, r), x);
-          y = fmaf(a.lora_scale, dot_r(B + r, t + r, r), y);
+          const float* ta = a.tgu + static_cast<size_t>(sl) * 2 * r;
+          x = fmaf(a.lora_scale, dot_r(B, ta, r), x);
+          y = fmaf(a.lora_scale, dot_r(B + r, ta + r, r), y);
         }
         store_h(a, sl, j, x, y);
       }
       __syncwarp();
     };
-    int i = ub;
-    if (ub < ue) columns();
-    // one more turn after the last unit: the barrier, and the item that the warp began and others went on with
+    bool open = false;  // the warp began the item and others go on with it
 #pragma unroll 1
-    for (;;) {
-      bool whole = false;
-      if (i < ue) {
-        copy_next();
-        cp_wait<kBuf - 1>();
-        gate_up_unit(rd, col + at.u * 512, ua + 4 * at.u, uc + 4 * at.u, acc);
-        if ((rd += kUnitBytes) == ring + kBuf * kUnitBytes) rd = ring;
+    while (left > 0) {
+      const int d = t >> logt, s0 = start[d], cl = start[d + 1] - 1, c0 = s0 + b;
+      const uint8_t* col = img + static_cast<size_t>(slots[min(c0 + g, cl)] >> 16) * ldu;
+      const float* ua = us + (slots[min(c0 + 2 * tig, cl)] >> 16) * G;
+      const float* uc = us + (slots[min(c0 + 2 * tig + 1, cl)] >> 16) * G;
+      const bool mine = u == 0;
+      const int end = min(U, u + left);
+      left -= end - u;
+      // where the units after these come from
+      const bool next_tile = c0 + 8 > cl;
+      const uint8_t* after = left > 0 && next_tile ? records(t + 1) : base;
+#pragma unroll 1
+      for (; u < end; ++u) {
+        const bool last = u + 1 == end;
+        const int n = last ? 0 : u + 1;
+        flip ^= 1;
+        if (!last || left > 0) copy(last ? after : base, n, (n & 1) == 0, flip);
+        cp_commit();
+        cp_wait<1>();
+        gate_up_unit(ring + (flip ^ 1) * kUnitBytes, set + 8 * (u & 1), plan.half(), col + u * 512, ua + 4 * u, uc + 4 * u, acc);
+        if (((u & 1) || U == 1) && (set += plan.set_bytes()) == sets + kSetsBytes) set = sets;
         __syncwarp();
-        ++i;
-        whole = ++at.u == U;
-        if (!whole && i < ue) continue;
-        if (!mine) {
-          part[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        }
+      }
+      if (!mine) {
+        part[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      } else if (end < U) {
+        open = true;
+        break;
       } else {
-        if (ub == ue) part[warp * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-        named_sync(15, kThreads);
-        if (ub == ue || !mine || at.u == 0) break;
-        const int end = ue + U - at.u;  // of the item
+        finish();
+      }
+      acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+      u = 0;
+      b = next_tile ? 0 : b + 8;
+      t += next_tile;
+      base = after;
+    }
+    if (ub == ue) part[warp * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    named_sync(15, kThreads);
+    if (open) {
+      const int end = ue + U - u;  // of the item
 #pragma unroll 2
-        for (int w = warp + 1; w < kWarps && border(w) < end; ++w) {
-          const float4 v = part[w * 32 + lane];
-          acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
-        }
-        whole = true;
+      for (int w = warp + 1; w < kWarps && border(w) < end; ++w) {
+        const float4 v = part[w * 32 + lane];
+        acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
       }
-      if (whole) {
-        if (mine) finish();
-        if (i >= ue && at.u != U) break;  // joined
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        mine = true;
-        at.u = 0;
-        at.b += 8;
-        if (at.b >= cnt) at.b = 0, ++at.t;
-        if (i < ue) columns();
-      }
+      finish();
     }
   }
   grid_arrive(a.bar, B_HIDDEN);
@@ -1068,32 +1075,31 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   const int Wd = 1 << logWd, teams = kWarps >> logWd, wi = warp & (Wd - 1);
   const int u0 = wi * (U2 >> logWd), u1 = u0 + (U2 >> logWd);
   plan.make(RDN, G2, 1, 8);
-  int ie = warp >> logWd, iu = u0;  // next to copy
-  uint32_t wr = ring32;
-  uint8_t* rd = ring;
-  const uint8_t* ibase = nullptr;
-  int in = 0;
-  auto open = [&]() {
-    const int rt = ie < nel ? 0 : 1, d = els[ie - rt * nel] & 511;
-    in = min(rt_rows, ndr - rt * rt_rows);
-    ibase = (d == 511 ? a.shared : a.pool + dist[d] * a.stride) + dn_off + static_cast<size_t>(dr0 + rt * rt_rows) * RDN;
+  // where the rows of element e (and how many of them) come from
+  auto rows_of = [&](int e) {
+    const int rt = e < nel ? 0 : 1, d = els[e - rt * nel] & 511;
+    return (d == 511 ? a.shared : a.pool + dist[d] * a.stride) + dn_off + static_cast<size_t>(dr0 + rt * rt_rows) * RDN;
   };
-  if (ie < total) open();
-  auto copy_next = [&]() {
-    if (ie < total) {
-      issue_unit(wr, plan, ibase + 128 * iu, ibase + 8 * iu, min(8, in), in - 8);
-      if (++iu == u1) {
-        iu = u0;
-        ie += teams;
-        if (ie < total) open();
-      }
+  uint32_t wset = sets32, flip = 0;
+  auto copy = [&](const uint8_t* from, int e, int unit, bool scales, uint32_t buf) {
+    const int n = e < nel ? rt_rows : ndr - rt_rows;
+    issue_codes(ring32 + buf * kUnitBytes, plan, from, unit, min(8, n), n - 8);
+    if (scales) {
+      issue_scales(wset, plan, from, unit, min(8, n), n - 8);
+      if ((wset += plan.set_bytes()) == sets32 + kSetsBytes) wset = sets32;
     }
-    cp_commit();
-    if ((wr += kUnitBytes) == ring32 + kBuf * kUnitBytes) wr = ring32;
   };
+  int ei = warp >> logWd;
+  const uint8_t* base = a.shared;
   cp_wait<0>();
-#pragma unroll 1
-  for (int i = 0; i < kBuf - 1; ++i) copy_next();
+  for (int i = 0; i < 2; ++i)  // row 15 of the buffers
+    *reinterpret_cast<uint32_t*>(ring + i * kUnitBytes + 15 * 128 + 4 * lane) = 0xffffffffu;
+  __syncwarp();
+  if (ei < total) {
+    base = rows_of(ei);
+    copy(base, ei, u0, true, 0);
+  }
+  cp_commit();
   if (a.shA[2] && warp < ndr && lane < (r * 2 + 127) / 128)
     asm volatile("prefetch.global.L1 [%0];" ::"l"(a.shB[2] + static_cast<size_t>(dr0 + warp) * r + 64 * lane));
   grid_wait(a.bar, B_HIDDEN, !a.exA, failed, a.err, a.timeout_ns);
@@ -1131,37 +1137,37 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   }
 
   {
-    int i = warp >> logWd, el = 0;
-    const uint8_t* col = nullptr;
-    auto column = [&]() {
-      el = els[i < nel ? i : i - nel];
-      const int cs = ((el >> 9) & 511) + min(g >> 1, (el >> 20) - 1);
-      col = hb + (static_cast<size_t>((el & 511) == 511 ? TK + cs : slots[cs] & 0xffff) * 2 + (g & 1)) * hrow;
-    };
-    if (i < total) column();
-    int u = u0;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint8_t* set = sets;
 #pragma unroll 1
-    while (i < total) {
-      const Frag f0 = load_frag(col + u * 512, 0), f1 = load_frag(col + u * 512, 1);
-      copy_next();
-      cp_wait<kBuf - 1>();
-      down_unit(rd, f0, f1, col + u * 512, G2 >= 4, acc);
-      if ((rd += kUnitBytes) == ring + kBuf * kUnitBytes) rd = ring;
-      if (++u == u1) {
-        u = u0;
-        const int s0 = (el >> 9) & 511;
-        if (tig < el >> 20) {
-          const int p = (el & 511) == 511 ? TK + s0 + tig : slots[s0 + tig] & 0xffff;
-          float* y = scratch + (wi * NS + p) * RS + (i < nel ? 0 : 16);
-          y[g] = fmaf(acc[1], 0x1p-11f, acc[0]) * 0x1p22f;
-          if (g < 7) y[g + 8] = fmaf(acc[3], 0x1p-11f, acc[2]) * 0x1p22f;
-        }
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-        i += teams;
-        if (i < total) column();
+    while (ei < total) {
+      const int el = els[ei < nel ? ei : ei - nel], s0 = (el >> 9) & 511, n = el >> 20;
+      const bool sh = (el & 511) == 511;
+      const int cs = s0 + min(g >> 1, n - 1);
+      const uint8_t* col = hb + (static_cast<size_t>(sh ? TK + cs : slots[cs] & 0xffff) * 2 + (g & 1)) * hrow;
+      const int ne = ei + teams;
+      const uint8_t* after = ne < total ? rows_of(ne) : base;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int u = u0; u < u1; ++u) {
+        const Frag f0 = load_frag(col + u * 512, 0), f1 = load_frag(col + u * 512, 1);
+        const bool last = u + 1 == u1;
+        const int nu = last ? u0 : u + 1;
+        flip ^= 1;
+        if (!last || ne < total) copy(last ? after : base, last ? ne : ei, nu, last || (nu & 1) == 0, flip);
+        cp_commit();
+        cp_wait<1>();
+        down_unit(ring + (flip ^ 1) * kUnitBytes, set + 8 * (u & 1), plan.half(), f0, f1, col + u * 512, G2 >= 4, acc);
+        if (((u & 1) || last) && (set += plan.set_bytes()) == sets + kSetsBytes) set = sets;
+        __syncwarp();
       }
-      __syncwarp();
+      if (tig < n) {
+        const int p = sh ? TK + s0 + tig : slots[s0 + tig] & 0xffff;
+        float* y = scratch + (wi * NS + p) * RS + (ei < nel ? 0 : 16);
+        y[g] = fmaf(acc[1], 0x1p-11f, acc[0]) * 0x1p22f;
+        if (g < 7) y[g + 8] = fmaf(acc[3], 0x1p-11f, acc[2]) * 0x1p22f;
+      }
+      ei = ne;
+      base = after;
     }
   }
   if (a.exA)

@@ -1373,7 +1373,7 @@ bool plan_layer(ld::Smem* s, const moe_layer* L, int T, int K, int grid, bool sm
   s->td = put((t > 96 ? t : 96) * ld::kMaxR * 4);  // partial sums of up to 24 (block, tile, part)s of 4 tokens
   s->red = put(2 * ld::kWarps * 8);
   s->misc = put(128);
-  s->ring = put(ld::kWarps * ld::kBuf * ld::kUnitBytes);
+  s->ring = put(ld::kWarps * ld::kWarpRing);
   s->total = static_cast<int>(o);
   return o <= 227 * 1024 && nrt <= 2 && cdiv(L->I, grid) <= ld::kMaxSharedPairs && cdiv(L->E + 1 + 2 * r, grid) <= 8;
 }

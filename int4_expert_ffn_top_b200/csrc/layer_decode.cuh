@@ -33,12 +33,13 @@ namespace ld {
 using tc::gtime;
 using tc::sa;
 
-constexpr int kWarps = 24;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxT = 32, kMaxK = 8, kMaxSlots = kMaxT * kMaxK, kMaxE = 256, kMaxR = 32;
 constexpr int kDownRows = 15;  // down: row 15 of the MMA tile sums the hidden values
 constexpr int kSlotBlock = 4;  // down: slots per MMA (hi and lo columns)
 constexpr int kMaxEls = kMaxSlots + kMaxT / kSlotBlock;
+constexpr int kRowGroups = (4096 / 64 + kWarps - 1) / kWarps;  // groups of a row over all tokens a warp takes
 constexpr int kMaxSharedPairs = 16;  // pairs of the shared expert a CTA takes
 constexpr int kHeaderBytes = 256;
 constexpr int kUnitBytes = 16 * 128, kSetsBytes = 1024;  // see UnitPlan
@@ -694,14 +695,14 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     }
     cp_commit();
   }
-  const int g0 = warp * G / kWarps, g1 = (warp + 1) * G / kWarps;  // groups of the rows over all tokens: up to 3
-  uint4 q8[3];
-  uint32_t sb8[3];  // scale and bias
+  const int g0 = warp * G / kWarps, g1 = (warp + 1) * G / kWarps;  // groups of the rows over all tokens
+  uint4 q8[kRowGroups];
+  uint32_t sb8[kRowGroups];  // scale and bias
   if (n8 > 0) {
     const int row = r0 + min(g, n8 - 1);
     const uint8_t* rec = row < a.E ? a.router + static_cast<size_t>(row) * R8 : a.sgate;
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < kRowGroups; ++i)
       if (g0 + i < g1) {
         q8[i] = __ldg(reinterpret_cast<const uint4*>(rec + (g0 + i) * 64 + tig * 16));
         const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + a.H) + g0 + i;
@@ -737,7 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     for (int i = tid; i < T * G; i += kThreads) us[i] = __ldcg(a.us + i);
     if (tid < T) ic[tid] = __ldcg(a.ic + tid);
   } else {
-    const int logW = T == 1 ? 4 : (T == 2 ? 3 : 2), W = 1 << logW, team = warp >> logW;  // at most 4 tokens
+    int logW = 0;  // at most 4 tokens
+    while (T << (logW + 1) <= kWarps) ++logW;
+    const int W = 1 << logW, team = warp >> logW;
     if (team < T)
       build(team, warp & (W - 1), W, team, sm + S.img + team * ldu, us + team * G, ic + team, team == cta);
   }
@@ -758,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
         const float* ua = us + min(8 * b + 2 * tig, T - 1) * G;
         const float* ub = us + min(8 * b + 2 * tig + 1, T - 1) * G;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kRowGroups; ++i) {
           const int gi = g0 + i;
           if (gi < g1) {
             const uint4* p = reinterpret_cast<const uint4*>(col + gi * 128 + tig * 32);
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
 #pragma unroll 1
     for (int task = warp; task < U * sh_ways; task += kWarps) {
       const int u = task & (U - 1);
-      if (ti > 0) {
+      if (ti > 0 || task >= kWarps) {
         const uint8_t* src = a.shared + static_cast<size_t>(2 * (sp0 + 8 * ti)) * RGU;
         const int n = min(8, nsp - 8 * ti);
         issue_codes(ring32, plan, src, u, n, n);
@@ -1176,11 +1179,12 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     named_sync(15, kThreads);
 
   // --------------------------------------------------------------------------- combine
-  const int t = tid >> 4;  // a thread per (token, row of a tile)
+  // a thread per (token, row of a tile)
 #pragma unroll 1
-  for (int rt = 0; rt < nrt && t < T; ++rt) {
-    const int row = rt * rt_rows + (tid & 15), o = rt * 16 + (tid & 15);
-    if ((tid & 15) >= rt_rows || row >= ndr) continue;
+  for (int i = tid; i < T * nrt * 16; i += kThreads) {
+    const int t = nrt > 1 ? i >> 5 : i >> 4, rt = nrt > 1 ? (i >> 4) & 1 : 0;
+    const int row = rt * rt_rows + (i & 15), o = rt * 16 + (i & 15);
+    if ((i & 15) >= rt_rows || row >= ndr) continue;
     const int hr = dr0 + row;
     float out = 0.f;
 #pragma unroll 1
@@ -1197,12 +1201,12 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
         if (a.shA[2]) {
           float l = 0.f;
 #pragma unroll 1
-          for (int i = 0; i < r; i += 8) {
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(a.shB[2] + static_cast<size_t>(hr) * r + i));
+          for (int k8 = 0; k8 < r; k8 += 8) {
+            const uint4 b = __ldg(reinterpret_cast<const uint4*>(a.shB[2] + static_cast<size_t>(hr) * r + k8));
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
             for (int w = 0; w < 1 << logp; ++w) {
-              const float4* p = reinterpret_cast<const float4*>(td + (w * T + t) * kMaxR + i);
+              const float4* p = reinterpret_cast<const float4*>(td + (w * T + t) * kMaxR + k8);
               const float4 x = p[0], z = p[1];
               v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += z.x, v[5] += z.y, v[6] += z.z, v[7] += z.w;
             }

@@ -327,7 +327,8 @@ typedef struct {
                           <= 0: 1 s for the single launch, 2 s for the GEMMs */
   int32_t path;        /* 0: automatic; 1: per-layer launches; 2: single-launch kernel (MOE_ERR_UNSUPPORTED if
                           the shapes are not eligible); 3: the first-generation single-launch kernel (kept for
-                          comparison) */
+                          comparison); 4: per layer, norm to combine in one moe_layer_decode launch
+                          (T <= MOE_LAYER_DECODE_MAX_TOKENS, else MOE_ERR_UNSUPPORTED) */
   int32_t test_drop_layer;  /* test hook for the timeout path, 0 = off; L > 0: on the single-launch path CTA */
   int32_t test_drop_cta;    /*   test_drop_cta never publishes its residual rows of layer L-1, so the other CTAs'
                                  bounded waits run out; on the per-layer path the CTA test_drop_cta of layer L-1's

@@ -404,7 +404,7 @@ def moe_stack_workspace_size(stack: StackStructs, T: int, K: int, K_next: int) -
     return lib().moe_stack_workspace_size(stack.layers, stack.heads_ptr(), stack.n, T, K, K_next)
 
 
-PATH_AUTO, PATH_LAYERS, PATH_SINGLE = 0, 1, 2
+PATH_AUTO, PATH_LAYERS, PATH_SINGLE, PATH_LAYER_DECODE = 0, 1, 2, 4
 
 
 def stack_opts(timeout_ns: int = 0, path: int = PATH_AUTO, drop_layer: int = -1, drop_cta: int = -1,

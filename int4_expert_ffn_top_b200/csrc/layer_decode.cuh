@@ -563,7 +563,7 @@ __device__ __noinline__ float dot_r(const uint16_t* B, const float* t, int r) {
 MOE_DEV void f16_rows(const uint16_t* ra, const uint16_t* rb, int g0, int g1, const uint8_t* col, float (&v)[4]) {
   const int tig = threadIdx.x & 3;
   float ev[4] = {0.f, 0.f, 0.f, 0.f}, od[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll 4
   for (int gi = g0; gi < g1; ++gi) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -633,7 +633,7 @@ __device__ __noinline__ void route_token(const Args& a, int t, int* sel, float* 
     const int s = t * K + lane;
     sel[s] = my_e;
     sw[s] = ex / den;
-    atomicOr(mask + my_e * 8 + (s >> 5), 1u << (s & 31));
+    atomicOr(mask + (s >> 5) * kMaxE + my_e, 1u << (s & 31));
     if (write) a.w[s] = ex / den;
   }
 }
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     const int first = kind ? r0 + n8 : r0, n = kind ? r1 - first : n8;
     if (n <= 0) continue;
     const int row = first + min(g, n - 1);
-#pragma unroll 1
+#pragma unroll 2
     for (int b = 0; b < nblk; ++b) {
       const uint8_t* col = img + static_cast<size_t>(min(8 * b + g, T - 1)) * ldu;
       float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   }
 
   // --------------------------------------------------------------------------- top-K, gating, the expert list
-  uint32_t* mask = reinterpret_cast<uint32_t*>(scratch);  // [256 experts][8 words]: the slots that chose an expert
+  uint32_t* mask = reinterpret_cast<uint32_t*>(scratch);  // [8 words][256 experts]: the slots that chose an expert
   for (int i = tid; i < kMaxE * 2; i += kThreads) reinterpret_cast<uint4*>(mask)[i] = make_uint4(0, 0, 0, 0);
   grid_wait(a.bar, B_LOGITS, false, failed, a.err, a.timeout_ns);
 #pragma unroll 1
@@ -857,47 +857,66 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   if (tid >= kThreads - 32 && lane < T) gate[lane] = sigmoid(__ldcg(a.aux + lane * (4 + 2 * r)));
   named_sync(15, kThreads);
   if (warp < 8) {  // chosen experts in ascending order, their slots in ascending order, the down elements
+    uint32_t m[8];
     int cnt = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cnt += __popc(mask[tid * 8 + i]);
+    for (int i = 0; i < 8; ++i) {
+      m[i] = 32 * i < TK ? mask[i * kMaxE + tid] : 0u;
+      cnt += __popc(m[i]);
+    }
     const uint32_t bal = __ballot_sync(0xffffffffu, cnt > 0);
-    int v = cnt | ((cnt + kSlotBlock - 1) / kSlotBlock) << 16;
-    const int own = v;
+    // slots | elements << 10 | experts << 20, summed over the experts before
+    const int own = cnt | ((cnt + kSlotBlock - 1) / kSlotBlock) << 10;
+    int v = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += y;
     }
-    int* tot = misc + 4;  // [8][2]
-    if (lane == 31) tot[2 * warp] = v, tot[2 * warp + 1] = __popc(bal);
+    int* tot = misc + 4;  // [8]
+    if (lane == 31) tot[warp] = v + (__popc(bal) << 20);
     named_sync(1, 256);
-    int off = v - own, d = __popc(bal & ((1u << lane) - 1));
-#pragma unroll 1
-    for (int w = 0; w < warp; ++w) off += tot[2 * w], d += tot[2 * w + 1];
-    int so = off & 0xffff, eo = sh_blocks + (off >> 16);
+    int off = v - own + (__popc(bal & ((1u << lane) - 1)) << 20);
+#pragma unroll
+    for (int w = 0; w < 7; ++w) off += w < warp ? tot[w] : 0;
+    const int d = off >> 20;
+    int so = off & 1023, eo = sh_blocks + ((off >> 10) & 1023);
     if (cnt > 0) {
       dist[d] = tid;
       start[d] = so;
 #pragma unroll 1
       for (int b = 0; b < cnt; b += kSlotBlock) els[eo++] = d | (so + b) << 9 | min(kSlotBlock, cnt - b) << 20;
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll 1
-        for (uint32_t m = mask[tid * 8 + i]; m; m &= m - 1) {
-          const int s = 32 * i + __ffs(m) - 1;
+        for (uint32_t q = m[i]; q; q &= q - 1) {
+          const int s = 32 * i + __ffs(q) - 1;
           slots[so++] = s | static_cast<int>(s * a.kmul >> 16) << 16;
         }
     }
     if (tid == 255) {
       const int D = d + (cnt > 0);
       misc[1] = D;
-      misc[2] = sh_blocks + (off >> 16) + (own >> 16);
+      misc[2] = sh_blocks + ((off >> 10) & 1023) + (own >> 10);
       start[D] = TK;
     }
     if (tid < sh_blocks) els[tid] = 511 | (tid * kSlotBlock) << 9 | min(kSlotBlock, T - tid * kSlotBlock) << 20;
   }
   named_sync(15, kThreads);
   const int D = misc[1], nel = misc[2];
+  if (a.exA) {  // the routed down adapters: this CTA's share of A, its rows of B for every slot, into L2 for later
+    const int logm = r > 16, lines = G2 * 16;  // of 16 rows of A
+#pragma unroll 1
+    for (int q = cta; q < (nel - sh_blocks) << logm; q += grid) {
+      const uint16_t* A = a.exA + (static_cast<size_t>(dist[els[sh_blocks + (q >> logm)] & 511]) * r + 16 * (q & logm)) * a.I;
+      const int n = min(lines, (r - 16 * (q & logm)) * G2);
+#pragma unroll 1
+      for (int i = tid; i < n; i += kThreads) prefetch_l2(A + i * 64);
+    }
+#pragma unroll 1
+    for (int s = warp; s < TK; s += kWarps)
+      if (lane < ndr) prefetch_l2(a.exB + (static_cast<size_t>(sel[s]) * a.H + dr0 + lane) * r);
+  }
 
   // --------------------------------------------------------------------------- routed gate/up adapters: A u
   if (a.exAgu) {
@@ -1173,12 +1192,27 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
       base = after;
     }
   }
+  if (a.exA) {
+#pragma unroll 1
+    for (int s = warp; s < TK; s += kWarps)
+      if (lane < ndr)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.exB + (static_cast<size_t>(sel[s]) * a.H + dr0 + lane) * r));
+  }
   if (a.exA)
     grid_wait(a.bar, B_EXDOWN, true, failed, a.err, a.timeout_ns);
   else
     named_sync(15, kThreads);
 
   // --------------------------------------------------------------------------- combine
+  if (a.shA[2] && logp > 0) {  // the parts of the shared down adapter's A h
+#pragma unroll 1
+    for (int i = tid; i < T * kMaxR; i += kThreads) {
+      float v = td[i];
+      for (int w = 1; w < 1 << logp; ++w) v += td[w * T * kMaxR + i];
+      td[i] = v;
+    }
+    named_sync(15, kThreads);
+  }
   // a thread per (token, row of a tile)
 #pragma unroll 1
   for (int i = tid; i < T * nrt * 16; i += kThreads) {
@@ -1203,13 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
 #pragma unroll 1
           for (int k8 = 0; k8 < r; k8 += 8) {
             const uint4 b = __ldg(reinterpret_cast<const uint4*>(a.shB[2] + static_cast<size_t>(hr) * r + k8));
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int w = 0; w < 1 << logp; ++w) {
-              const float4* p = reinterpret_cast<const float4*>(td + (w * T + t) * kMaxR + k8);
-              const float4 x = p[0], z = p[1];
-              v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += z.x, v[5] += z.y, v[6] += z.z, v[7] += z.w;
-            }
+            const float* v = td + t * kMaxR + k8;
             l = fmaf(lo_half(b.x), v[0], l), l = fmaf(hi_half(b.x), v[1], l);
             l = fmaf(lo_half(b.y), v[2], l), l = fmaf(hi_half(b.y), v[3], l);
             l = fmaf(lo_half(b.z), v[4], l), l = fmaf(hi_half(b.z), v[5], l);

@@ -804,6 +804,187 @@ moe_status prerouter_predict(const moe_prerouter* head, const uint16_t* u, const
 
 }  // extern "C"
 
+// ----------------------------------------------------------------------------- one layer, few tokens, one launch
+namespace {
+
+struct LayerWs {
+  ld::Header* bar;
+  uint8_t* img;
+  float *us, *ic, *logits, *aux, *tgu, *tex;
+  uint16_t* h;
+  size_t bytes;
+};
+
+LayerWs carve_layer(void* base, const moe_layer* L, int T, int K) {
+  LayerWs w{};
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t o = off;
+    off = align_up(off + n, 256);
+    return base ? static_cast<char*>(base) + o : nullptr;
+  };
+  const size_t t = static_cast<size_t>(T), TK = t * K, r = L->r > 0 ? L->r : 0;
+  w.bar = reinterpret_cast<ld::Header*>(take(ld::kHeaderBytes));
+  w.img = reinterpret_cast<uint8_t*>(take(t * (2 * L->H + 16)));
+  w.us = reinterpret_cast<float*>(take(t * (L->H / 64) * 4));
+  w.ic = reinterpret_cast<float*>(take(t * 4));
+  w.logits = reinterpret_cast<float*>(take(t * L->E * 4));
+  w.aux = reinterpret_cast<float*>(take(t * (4 + 2 * r) * 4));
+  w.h = reinterpret_cast<uint16_t*>(take((TK + t) * 2 * L->I * 2));
+  w.tgu = reinterpret_cast<float*>(take(L->ex_lora_A_gu ? TK * 2 * r * 4 : 0));
+  w.tex = reinterpret_cast<float*>(take(L->ex_lora_A ? TK * r * 4 : 0));
+  w.bytes = off;
+  return w;
+}
+
+// Shared-memory plan for a grid of `grid` CTAs; false if the shape does not fit.
+bool plan_layer(ld::Smem* s, const moe_layer* L, int T, int K, int grid, bool smem_image) {
+  const int H = L->H, G = H / 64;
+  auto cdiv = [](int a, int b) { return (a + b - 1) / b; };
+  size_t o = 0;
+  auto put = [&](size_t n) {
+    const size_t at = align_up(o, 128);
+    o = at + n;
+    return static_cast<int>(at);
+  };
+  const size_t t = static_cast<size_t>(T);
+  const int nrt = cdiv(cdiv(H, grid), ld::kDownRows), r = L->r > 0 ? L->r : 0;
+  size_t scratch = 2 * ld::kWarps * 32 * 16;  // partial sums of the gate/up teams; rows over all tokens: no more
+  const size_t y = (t * K + t) * nrt * 16 * 4, sh = static_cast<size_t>(cdiv(T, 8)) * (G / 4) * 512;
+  if (y > scratch) scratch = y;
+  if (sh > scratch) scratch = sh;
+  s->img = put(smem_image ? t * (2 * H + 16) : 0);
+  s->us = put(t * G * 4);
+  s->ic = put(t * 4);
+  s->scratch = put(scratch);
+  s->sraw = put(t * ld::kMaxSharedPairs * 8);
+  s->sel = put(ld::kMaxSlots * 4);
+  s->w = put(ld::kMaxSlots * 4);
+  s->dist = put(ld::kMaxE * 4);
+  s->start = put((ld::kMaxE + 1) * 4);
+  s->slots = put(ld::kMaxSlots * 4);
+  s->els = put(ld::kMaxEls * 4);
+  s->gate = put(t * 4);
+  s->td = put((t > 96 ? t : 96) * ld::kMaxR * 4);  // partial sums of up to 24 (block, tile, part)s of 4 tokens
+  s->red = put(2 * ld::kWarps * 8);
+  s->misc = put(128);
+  s->ring = put(ld::kWarps * ld::kWarpRing);
+  s->total = static_cast<int>(o);
+  return o <= 227 * 1024 && nrt <= 2 && cdiv(L->I, grid) <= ld::kMaxSharedPairs && cdiv(L->E + 1 + 2 * r, grid) <= 8;
+}
+
+// Multiprocessors of the current device, with the kernel's shared memory allowed there; 0 on failure.
+int layer_grid() {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaFuncSetAttribute(ld::layer_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
+            cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return 0;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// moe_layer_decode with the bound of its waits exposed (the stack passes its option through).
+moe_status layer_decode_entry(const moe_layer* L, uint16_t* u, const float* x, float eps, int32_t T, int32_t K,
+                              const int32_t* exec_idx, float* logits, int32_t* idx, float* w, void* out,
+                              int32_t out_mode, void* workspace, size_t ws_bytes, int32_t* err_word,
+                              long long timeout_ns, void* stream) {
+  moe_status s = check_layer(L, T, K);
+  if (s != MOE_OK) return s;
+  if (T > MOE_LAYER_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  if (out_mode < 0 || out_mode > 2 || (x && !(eps >= 0.f))) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if ((!u && !x) || !idx || !w || !out || (u && !aligned(u, 16)) || (x && !aligned(x, 16))) return MOE_ERR_INVALID_ARG;
+  s = check_expert_weights(L);
+  if (s != MOE_OK) return s;
+  if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  const LayerWs ws = carve_layer(workspace, L, T, K);
+  if (ws_bytes < ws.bytes) return MOE_ERR_WORKSPACE;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = layer_grid();
+  if (grid < 1) return MOE_ERR_CUDA;
+  ld::Args a{};
+  a.T = T;
+  a.K = K;
+  a.E = L->E;
+  a.H = L->H;
+  a.I = L->I;
+  while ((1 << a.logI) < L->I) ++a.logI;
+  while ((256 << a.logU) < L->H) ++a.logU;
+  a.gmul = static_cast<uint32_t>(((1ull << 32) + grid - 1) / grid);
+  a.kmul = (65536 + K - 1) / K;
+  a.r = L->r;
+  a.u = x ? nullptr : u;
+  a.x = x;
+  a.eps = eps;
+  a.inv_h = 1.0 / L->H;
+  a.u_out = x ? u : nullptr;
+  a.exec_idx = exec_idx;
+  a.logits = logits ? logits : ws.logits;
+  a.idx = idx;
+  a.w = w;
+  a.out = out;
+  a.out_mode = out_mode;
+  a.router = static_cast<const uint8_t*>(L->router.rows);
+  a.rbias = L->router_bias;
+  a.sgate = static_cast<const uint8_t*>(L->shared_gate.rows);
+  a.shared = static_cast<const uint8_t*>(L->shared_block);
+  if (L->r > 0) {
+    for (int p = 0; p < 3; ++p) {
+      a.shA[p] = L->sh_lora_A[p];
+      a.shB[p] = L->sh_lora_B[p];
+    }
+    a.exA = L->ex_lora_A;
+    a.exB = L->ex_lora_B;
+    a.exAgu = L->ex_lora_A_gu;
+    a.exBgu = L->ex_lora_B_gu;
+  }
+  a.lora_scale = L->lora_scale;
+  a.pool = static_cast<const uint8_t*>(L->pool);
+  a.stride = L->expert_stride;
+  a.bar = ws.bar;
+  a.img = ws.img;
+  a.us = ws.us;
+  a.ic = ws.ic;
+  a.aux = ws.aux;
+  a.h = ws.h;
+  a.tgu = ws.tgu;
+  a.tex = ws.tex;
+  a.err = err_word;
+  a.timeout_ns = timeout_ns;
+  a.smem_image = T <= 4;
+  if (!plan_layer(&a.sm, L, T, K, grid, a.smem_image)) return MOE_ERR_UNSUPPORTED;
+  void* args[] = {&a};
+  return cudaLaunchCooperativeKernel(reinterpret_cast<void*>(ld::layer_decode_kernel), dim3(grid), dim3(ld::kThreads),
+                                     args, a.sm.total, st) == cudaSuccess
+             ? MOE_OK
+             : (cudaGetLastError(), MOE_ERR_CUDA);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_layer_decode_workspace_size(const moe_layer* L, int32_t T, int32_t K) {
+  if (!L || T < 0 || T > MOE_LAYER_DECODE_MAX_TOKENS || K < 1) return 0;
+  return carve_layer(nullptr, L, T, K).bytes;
+}
+
+moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, float eps, int32_t T, int32_t K,
+                            const int32_t* exec_idx, float* logits, int32_t* idx, float* w, void* out, int32_t out_mode,
+                            void* workspace, size_t ws_bytes, int32_t* err_word, void* stream) {
+  return layer_decode_entry(L, u, x, eps, T, K, exec_idx, logits, idx, w, out, out_mode, workspace, ws_bytes, err_word,
+                            kGemmTimeoutNs, stream);
+}
+
+}  // extern "C"
+
 // ----------------------------------------------------------------------------- stacked decode
 namespace {
 
@@ -1174,6 +1355,10 @@ StackWs carve_stack(void* base, const moe_layer* L0, const moe_prerouter* P0, in
   w.err = reinterpret_cast<int32_t*>(take(4));
   w.ll = reinterpret_cast<unsigned long long*>(take(ll_bytes));
   w.ews_bytes = ws_bytes_for(L0, T, K);
+  if (T <= MOE_LAYER_DECODE_MAX_TOKENS) {  // path 4
+    const size_t one = carve_layer(nullptr, L0, T, K).bytes;
+    if (one > w.ews_bytes) w.ews_bytes = one;
+  }
   w.ews = take(w.ews_bytes);
   w.pws_bytes = P0 ? prerouter_ws(P0, T) : 0;
   w.pws = take(w.pws_bytes);
@@ -1212,7 +1397,8 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
                             void* stream) {
   if (!layers || n_layers < 1 || !x) return MOE_ERR_INVALID_ARG;
   if (use_predicted_routing && (!heads || K_next != K)) return MOE_ERR_INVALID_ARG;
-  if (opts && (opts->path < 0 || opts->path > 3)) return MOE_ERR_INVALID_ARG;
+  if (opts && (opts->path < 0 || opts->path > 4)) return MOE_ERR_INVALID_ARG;
+  if (opts && opts->path == 4 && T > MOE_LAYER_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
   for (int l = 0; l < n_layers; ++l) {
     const moe_status s = check_layer(&layers[l], T, K);
     if (s != MOE_OK) return s;
@@ -1278,25 +1464,33 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
     if (x_trace && cudaMemcpyAsync(x_trace + static_cast<size_t>(l) * T * H, x, static_cast<size_t>(T) * H * 4,
                                    cudaMemcpyDeviceToDevice, st) != cudaSuccess)
       return MOE_ERR_CUDA;
-    moe_status s = moe_rmsnorm_bf16(x, T, H, eps, u, stream);
-    if (s != MOE_OK) return s;
     int32_t* idx_true = true_idx_all ? true_idx_all + l * TK : (idx_all && !use_predicted_routing ? idx_all + l * TK
                                                                                                     : ws.idx_true);
-    s = moe_route_topk(L, u, T, K, ws.logits, idx_true, ws.w, err, stream);
-    if (s != MOE_OK) return s;
-    const int32_t* idx_exec = idx_true;
-    if (use_predicted_routing && l > 0) {
-      gate_at_kernel<<<(T + kWarps - 1) / kWarps, kThreads, 0, st>>>(ws.logits, T, E, K, pred_prev, ws.w);
-      idx_exec = pred_prev;
+    const int32_t* idx_exec = use_predicted_routing && l > 0 ? pred_prev : idx_true;
+    moe_status s;
+    if (want == 4) {
+      s = layer_decode_entry(L, u, x, eps, T, K, idx_exec == idx_true ? nullptr : idx_exec, ws.logits, idx_true, ws.w, x, 2,
+                             ws.ews, ws.ews_bytes, err,
+                             (opts && opts->timeout_ns > 0) ? opts->timeout_ns : kGemmTimeoutNs, stream);
+      if (s != MOE_OK) return s;
+    } else {
+      s = moe_rmsnorm_bf16(x, T, H, eps, u, stream);
+      if (s != MOE_OK) return s;
+      s = moe_route_topk(L, u, T, K, ws.logits, idx_true, ws.w, err, stream);
+      if (s != MOE_OK) return s;
+      if (idx_exec != idx_true)
+        gate_at_kernel<<<(T + kWarps - 1) / kWarps, kThreads, 0, st>>>(ws.logits, T, E, K, pred_prev, ws.w);
     }
     if (idx_all && idx_all + l * TK != idx_exec &&
         cudaMemcpyAsync(idx_all + l * TK, idx_exec, TK * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
       return MOE_ERR_CUDA;
-    const long long gemm_to = (opts && opts->timeout_ns > 0) ? opts->timeout_ns : kGemmTimeoutNs;
-    const int drop = (opts && opts->test_drop_layer == l + 1) ? opts->test_drop_cta : -1;
-    s = expert_forward_entry(L, u, T, K, idx_exec, ws.w, x, 2, nullptr, ws.ews, ws.ews_bytes, err, gemm_to, drop,
-                             stream);
-    if (s != MOE_OK) return s;
+    if (want != 4) {
+      const long long gemm_to = (opts && opts->timeout_ns > 0) ? opts->timeout_ns : kGemmTimeoutNs;
+      const int drop = (opts && opts->test_drop_layer == l + 1) ? opts->test_drop_cta : -1;
+      s = expert_forward_entry(L, u, T, K, idx_exec, ws.w, x, 2, nullptr, ws.ews, ws.ews_bytes, err, gemm_to, drop,
+                               stream);
+      if (s != MOE_OK) return s;
+    }
     if (heads) {
       int32_t* pred = pred_all ? pred_all + l * TKn : ((l & 1) ? ws.pred1 : ws.pred0);
       s = prerouter_predict(&heads[l], u, idx_exec, T, K, K_next, pred, ws.scores, ws.pws, ws.pws_bytes, err, stream);
@@ -1305,178 +1499,6 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
     }
   }
   return launch_status();
-}
-
-}  // extern "C"
-
-// ----------------------------------------------------------------------------- one layer, few tokens, one launch
-namespace {
-
-struct LayerWs {
-  ld::Header* bar;
-  uint8_t* img;
-  float *us, *ic, *logits, *aux, *tgu, *tex;
-  uint16_t* h;
-  size_t bytes;
-};
-
-LayerWs carve_layer(void* base, const moe_layer* L, int T, int K) {
-  LayerWs w{};
-  size_t off = 0;
-  auto take = [&](size_t n) {
-    const size_t o = off;
-    off = align_up(off + n, 256);
-    return base ? static_cast<char*>(base) + o : nullptr;
-  };
-  const size_t t = static_cast<size_t>(T), TK = t * K, r = L->r > 0 ? L->r : 0;
-  w.bar = reinterpret_cast<ld::Header*>(take(ld::kHeaderBytes));
-  w.img = reinterpret_cast<uint8_t*>(take(t * (2 * L->H + 16)));
-  w.us = reinterpret_cast<float*>(take(t * (L->H / 64) * 4));
-  w.ic = reinterpret_cast<float*>(take(t * 4));
-  w.logits = reinterpret_cast<float*>(take(t * L->E * 4));
-  w.aux = reinterpret_cast<float*>(take(t * (4 + 2 * r) * 4));
-  w.h = reinterpret_cast<uint16_t*>(take((TK + t) * 2 * L->I * 2));
-  w.tgu = reinterpret_cast<float*>(take(L->ex_lora_A_gu ? TK * 2 * r * 4 : 0));
-  w.tex = reinterpret_cast<float*>(take(L->ex_lora_A ? TK * r * 4 : 0));
-  w.bytes = off;
-  return w;
-}
-
-// Shared-memory plan for a grid of `grid` CTAs; false if the shape does not fit.
-bool plan_layer(ld::Smem* s, const moe_layer* L, int T, int K, int grid, bool smem_image) {
-  const int H = L->H, G = H / 64;
-  auto cdiv = [](int a, int b) { return (a + b - 1) / b; };
-  size_t o = 0;
-  auto put = [&](size_t n) {
-    const size_t at = align_up(o, 128);
-    o = at + n;
-    return static_cast<int>(at);
-  };
-  const size_t t = static_cast<size_t>(T);
-  const int nrt = cdiv(cdiv(H, grid), ld::kDownRows), r = L->r > 0 ? L->r : 0;
-  size_t scratch = 2 * ld::kWarps * 32 * 16;  // partial sums of the gate/up teams; rows over all tokens: no more
-  const size_t y = (t * K + t) * nrt * 16 * 4, sh = static_cast<size_t>(cdiv(T, 8)) * (G / 4) * 512;
-  if (y > scratch) scratch = y;
-  if (sh > scratch) scratch = sh;
-  s->img = put(smem_image ? t * (2 * H + 16) : 0);
-  s->us = put(t * G * 4);
-  s->ic = put(t * 4);
-  s->scratch = put(scratch);
-  s->sraw = put(t * ld::kMaxSharedPairs * 8);
-  s->sel = put(ld::kMaxSlots * 4);
-  s->w = put(ld::kMaxSlots * 4);
-  s->dist = put(ld::kMaxE * 4);
-  s->start = put((ld::kMaxE + 1) * 4);
-  s->slots = put(ld::kMaxSlots * 4);
-  s->els = put(ld::kMaxEls * 4);
-  s->gate = put(t * 4);
-  s->td = put((t > 96 ? t : 96) * ld::kMaxR * 4);  // partial sums of up to 24 (block, tile, part)s of 4 tokens
-  s->red = put(2 * ld::kWarps * 8);
-  s->misc = put(128);
-  s->ring = put(ld::kWarps * ld::kWarpRing);
-  s->total = static_cast<int>(o);
-  return o <= 227 * 1024 && nrt <= 2 && cdiv(L->I, grid) <= ld::kMaxSharedPairs && cdiv(L->E + 1 + 2 * r, grid) <= 8;
-}
-
-// Multiprocessors of the current device, with the kernel's shared memory allowed there; 0 on failure.
-int layer_grid() {
-  constexpr int kMaxDev = 64;
-  static std::atomic<int> known[kMaxDev];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
-  int n = known[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaFuncSetAttribute(ld::layer_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-            cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return 0;
-    known[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-}  // namespace
-
-extern "C" {
-
-size_t moe_layer_decode_workspace_size(const moe_layer* L, int32_t T, int32_t K) {
-  if (!L || T < 0 || T > MOE_LAYER_DECODE_MAX_TOKENS || K < 1) return 0;
-  return carve_layer(nullptr, L, T, K).bytes;
-}
-
-moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, float eps, int32_t T, int32_t K,
-                            const int32_t* exec_idx, float* logits, int32_t* idx, float* w, void* out, int32_t out_mode,
-                            void* workspace, size_t ws_bytes, int32_t* err_word, void* stream) {
-  moe_status s = check_layer(L, T, K);
-  if (s != MOE_OK) return s;
-  if (T > MOE_LAYER_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
-  if (out_mode < 0 || out_mode > 2 || (x && !(eps >= 0.f))) return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
-  if ((!u && !x) || !idx || !w || !out || (u && !aligned(u, 16)) || (x && !aligned(x, 16))) return MOE_ERR_INVALID_ARG;
-  s = check_expert_weights(L);
-  if (s != MOE_OK) return s;
-  if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
-  const LayerWs ws = carve_layer(workspace, L, T, K);
-  if (ws_bytes < ws.bytes) return MOE_ERR_WORKSPACE;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = layer_grid();
-  if (grid < 1) return MOE_ERR_CUDA;
-  ld::Args a{};
-  a.T = T;
-  a.K = K;
-  a.E = L->E;
-  a.H = L->H;
-  a.I = L->I;
-  while ((1 << a.logI) < L->I) ++a.logI;
-  while ((256 << a.logU) < L->H) ++a.logU;
-  a.gmul = static_cast<uint32_t>(((1ull << 32) + grid - 1) / grid);
-  a.kmul = (65536 + K - 1) / K;
-  a.r = L->r;
-  a.u = x ? nullptr : u;
-  a.x = x;
-  a.eps = eps;
-  a.inv_h = 1.0 / L->H;
-  a.u_out = x ? u : nullptr;
-  a.exec_idx = exec_idx;
-  a.logits = logits ? logits : ws.logits;
-  a.idx = idx;
-  a.w = w;
-  a.out = out;
-  a.out_mode = out_mode;
-  a.router = static_cast<const uint8_t*>(L->router.rows);
-  a.rbias = L->router_bias;
-  a.sgate = static_cast<const uint8_t*>(L->shared_gate.rows);
-  a.shared = static_cast<const uint8_t*>(L->shared_block);
-  if (L->r > 0) {
-    for (int p = 0; p < 3; ++p) {
-      a.shA[p] = L->sh_lora_A[p];
-      a.shB[p] = L->sh_lora_B[p];
-    }
-    a.exA = L->ex_lora_A;
-    a.exB = L->ex_lora_B;
-    a.exAgu = L->ex_lora_A_gu;
-    a.exBgu = L->ex_lora_B_gu;
-  }
-  a.lora_scale = L->lora_scale;
-  a.pool = static_cast<const uint8_t*>(L->pool);
-  a.stride = L->expert_stride;
-  a.bar = ws.bar;
-  a.img = ws.img;
-  a.us = ws.us;
-  a.ic = ws.ic;
-  a.aux = ws.aux;
-  a.h = ws.h;
-  a.tgu = ws.tgu;
-  a.tex = ws.tex;
-  a.err = err_word;
-  a.timeout_ns = kGemmTimeoutNs;
-  a.smem_image = T <= 4;
-  if (!plan_layer(&a.sm, L, T, K, grid, a.smem_image)) return MOE_ERR_UNSUPPORTED;
-  void* args[] = {&a};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<void*>(ld::layer_decode_kernel), dim3(grid), dim3(ld::kThreads),
-                                     args, a.sm.total, st) == cudaSuccess
-             ? MOE_OK
-             : (cudaGetLastError(), MOE_ERR_CUDA);
 }
 
 }  // extern "C"

@@ -433,3 +433,63 @@ def test_projection_then_layer(cuda_ok, T):
         out = definition(L, normed(after), 4)[3]
         assert rel(mids[2 * i + 1], after.double() + out) <= OUT_TOL + 1e-5
         before = mids[2 * i + 1]
+
+
+# ----------------------------------------------------------------------------- as a path of the stack
+@pytest.mark.parametrize("T,predicted", [(1, False), (3, True), (9, False), (32, True)])
+def test_stack_path(cuda_ok, T, predicted):
+    """moe_stack_decode with one launch a layer: every layer's step from the traces, against 64 bits; the Prerouter's
+    predictions as the per-layer path makes them."""
+    H, E, I, K, P = 512, 24, 256, 4, 64
+    layers = [Layer(H, E, I, 16, down=True, seed=s) for s in range(3)]
+    g = torch.Generator(device=DEV).manual_seed(11)
+
+    class Head:
+        def __init__(self):
+            self.t = {n: (torch.randn(sh, device=DEV, generator=g) / sh[-1] ** 0.5).half()
+                      for n, sh in (("W1", (P, H + E)), ("b1", (P,)), ("W2", (E, P)), ("b2", (E,)))}
+            self.struct = _lib.moe_prerouter(*(self.t[n].data_ptr() for n in ("W1", "b1", "W2", "b2")), H, E, P, E)
+
+    heads = [Head() for _ in layers]
+    st = M.StackStructs([l.dev for l in layers], heads)
+    n = len(layers)
+
+    def run(path):
+        x = tokens(T, H)
+        o = dict(x_trace=torch.zeros((n, T, H), device=DEV), u_trace=torch.zeros((n, T, H), dtype=torch.bfloat16, device=DEV),
+                 idx_all=torch.zeros((n, T, K), dtype=torch.int32, device=DEV),
+                 true_idx_all=torch.zeros((n, T, K), dtype=torch.int32, device=DEV),
+                 pred_all=torch.zeros((n, T, K), dtype=torch.int32, device=DEV))
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        ws = M.workspace(M.moe_stack_workspace_size(st, T, K, K))
+        ws.fill_(0xC3)
+        M.moe_stack_decode(st, x, K, K, EPS, ws, use_predicted_routing=predicted, err_word=err,
+                           opts=M.stack_opts(path=path), **o)
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        return x, o
+
+    x, o = run(M.PATH_LAYER_DECODE)
+    _, ref = run(M.PATH_LAYERS)
+    assert torch.equal(o["u_trace"][0], ref["u_trace"][0]) and torch.equal(o["true_idx_all"][0], ref["true_idx_all"][0])
+    assert torch.equal(o["pred_all"][0], ref["pred_all"][0])
+    for l, L in enumerate(layers):
+        before, after = o["x_trace"][l], o["x_trace"][l + 1] if l + 1 < n else x
+        u = o["u_trace"][l]
+        assert torch.equal(u, normed(before))
+        ex = o["pred_all"][l - 1] if predicted and l else o["true_idx_all"][l]
+        assert torch.equal(o["idx_all"][l], ex)
+        out = definition(L, u, K, ex)[3]
+        # the layer's tolerance, and the sum's rounding relative to the sum
+        tol = OUT_TOL + 1e-5 + EPS32 * (after.double().norm(dim=1) / out.norm(dim=1)).max().item()
+        assert rel(after.double() - before.double(), out) <= tol
+
+
+def test_stack_path_refuses_many_tokens(cuda_ok):
+    L = Layer(256, 16, 128, 8)
+    st = M.StackStructs([L.dev])
+    x = torch.zeros((33, 256), device=DEV)
+    with pytest.raises(M.MoEError) as e:
+        M.moe_stack_decode(st, x, 2, 2, EPS, M.workspace(M.moe_stack_workspace_size(st, 33, 2, 2)),
+                           opts=M.stack_opts(path=M.PATH_LAYER_DECODE))
+    assert e.value.code == _lib.MOE_ERR_UNSUPPORTED

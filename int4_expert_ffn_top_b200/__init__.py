@@ -28,9 +28,9 @@ def lib() -> ctypes.CDLL:
     return _lib.load()
 
 
-def _stream(stream, dev: int | None = None) -> int:
-    if stream is None:  # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
+def _stream(stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -67,20 +67,6 @@ def _arg(fn: str, name: str, t, dtypes, numel: int = 0, optional: bool = False) 
     if t.device.index != torch.cuda.current_device():
         raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return t.data_ptr()
-
-
-def _fast(t, dtypes, numel: int, dev: int) -> int | None:
-    """Address of a tensor that passes every check of :func:`_arg` on device number ``dev``; None otherwise.
-
-    The calls for a few tokens go through this first: their time on the host is mostly argument checks.
-    """
-    try:
-        d = t.device
-        if t.dtype in dtypes and t.numel() >= numel and d.type == "cuda" and d.index == dev and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    return None
 
 
 def _rows(fn: str, name: str, t, width: int, dtypes) -> int:
@@ -168,25 +154,21 @@ def moe_layer_decode(layer: DeviceLayer, u: torch.Tensor | None, K: int, idx: to
     or is None.  ``exec_idx`` executes these experts instead of the router's own top-K, which ``idx`` receives.
     """
     fn, L = "moe_layer_decode", layer.struct
-    rows = u if x is None else x
-    H = L.H
-    if not isinstance(rows, torch.Tensor) or rows.dim() != 2 or rows.shape[1] != H:
-        _rows(fn, "u" if x is None else "x", rows, H, BF16_BITS if x is None else F32)
-    T = rows.shape[0]
-    dev = torch.cuda.current_device()
-
-    def ptr(name, t, dtypes, n):
-        return _fast(t, dtypes, n, dev) or _arg(fn, name, t, dtypes, n)
-
-    pu = None if u is None else ptr("u", u, BF16_BITS, T * H)
-    px = None if x is None else ptr("x", x, F32, T * H)
-    code = lib().moe_layer_decode(
-        ctypes.byref(L), pu, px, eps, T, K, None if exec_idx is None else ptr("exec_idx", exec_idx, I32, T * K),
-        None if logits is None else ptr("logits", logits, F32, T * L.E), ptr("idx", idx, I32, T * K),
-        ptr("w", w, F32, T * K), ptr("out", out, BF16_BITS if out_mode == OUT_BF16 else F32, T * H), out_mode,
-        *_ws(fn, workspace), None if err_word is None else ptr("err_word", err_word, I32, 1), _stream(stream, dev))
-    if code:
-        _check(fn, code)
+    if stream is None:
+        code = _lib.binding().layer(ctypes.addressof(L), u, x, eps, K, exec_idx, logits, idx, w, out, out_mode, workspace,
+                                    err_word)
+        if code is not None:
+            return _check(fn, code)
+    if x is None:
+        T = _rows(fn, "u", u, L.H, BF16_BITS)
+    else:
+        T = _rows(fn, "x", x, L.H, F32)
+    _check(fn, lib().moe_layer_decode(
+        ctypes.byref(L), _arg(fn, "u", u, BF16_BITS, T * L.H, optional=x is not None), _p(x), eps, T, K,
+        _arg(fn, "exec_idx", exec_idx, I32, T * K, optional=True), _arg(fn, "logits", logits, F32, T * L.E, optional=True),
+        _arg(fn, "idx", idx, I32, T * K), _arg(fn, "w", w, F32, T * K),
+        _arg(fn, "out", out, BF16_BITS if out_mode == OUT_BF16 else F32, T * L.H), out_mode, *_ws(fn, workspace),
+        _arg(fn, "err_word", err_word, I32, 1, optional=True), _stream(stream)))
 
 
 def moe_noalloc_scratch_bytes() -> int:
@@ -235,12 +217,12 @@ def moe_i8_row_bytes(n: int) -> int:
     return lib().moe_i8_row_bytes(n)
 
 
-def _i8_rows(fn: str, name: str, q, width: int, dev: int) -> tuple[int, int, int]:
+def _i8_rows(fn: str, name: str, q, width: int) -> tuple[int, int, int]:
     """(address, row bytes, rows) of an 8-bit code tensor ``[T, ld]`` whose rows hold ``width`` codes."""
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise ValueError(f"{fn}: {name} must be [T, ld]")
     rows, ld = q.shape
-    p = _fast(q, I8, 0, dev) or _arg(fn, name, q, I8)
+    p = _arg(fn, name, q, I8)
     if ld % 16 or ld < width:
         raise ValueError(f"{fn}: {name} rows hold {ld} bytes, need a multiple of 16 that holds {width}")
     return p, ld, rows
@@ -252,6 +234,10 @@ def moe_quant_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, eps: flo
     ``q`` int8 ``[T, ld]`` with ``ld`` a multiple of 16 (``moe_i8_row_bytes(H)`` or more), ``scale`` fp32 ``[T]``.
     """
     fn = "moe_quant_i8"
+    if stream is None:
+        code = _lib.binding().quant(x, q, scale, eps)
+        if code is not None:
+            return _check(fn, code)
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{fn}: x must be [T, H]")
     if eps is None:
@@ -259,34 +245,29 @@ def moe_quant_i8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, eps: flo
     elif not eps >= 0:
         raise ValueError(f"{fn}: eps must be >= 0, got {eps}")
     T, H = x.shape
-    dev = x.device.index
-    if dev is None or dev != torch.cuda.current_device():
-        _arg(fn, "x", x, F32_OR_BF16)
-    px = _fast(x, F32_OR_BF16, 0, dev) or _arg(fn, "x", x, F32_OR_BF16)
-    pq, ld, rows = _i8_rows(fn, "q", q, H, dev)
+    px = _arg(fn, "x", x, F32_OR_BF16)
+    pq, ld, rows = _i8_rows(fn, "q", q, H)
     if rows < T:
         raise ValueError(f"{fn}: q has {rows} rows, x has {T}")
-    ps = _fast(scale, F32, T, dev) or _arg(fn, "scale", scale, F32, T)
-    code = lib().moe_quant_i8(px, 1 if x.dtype is torch.bfloat16 else 0, T, H, eps, pq, ld, ps, _stream(stream, dev))
-    if code:
-        _check(fn, code)
+    ps = _arg(fn, "scale", scale, F32, T)
+    _check(fn, lib().moe_quant_i8(px, 1 if x.dtype is torch.bfloat16 else 0, T, H, eps, pq, ld, ps, _stream(stream)))
 
 
 def moe_linear_i8(linear: DeviceLinear8, q: torch.Tensor, qscale: torch.Tensor, out: torch.Tensor, out_mode: int,
                   err_word: torch.Tensor | None = None, stream=None):
     """``out [T, out_dim] = qscale[t] scale[n] sum_k q[t,k] codes[n,k] + bias[n]`` for the ``T`` rows of ``q``."""
     fn, W = "moe_linear_i8", linear.struct
-    dev = linear.device.index
-    if dev != torch.cuda.current_device():
+    if stream is None:
+        code = _lib.binding().linear(ctypes.addressof(W), linear.device.index, q, qscale, out, out_mode, err_word)
+        if code is not None:
+            return _check(fn, code)
+    if linear.device.index != torch.cuda.current_device():
         raise ValueError(f"{fn}: the matrix is on {linear.device}, the current device is cuda:{torch.cuda.current_device()}")
-    pq, ld, T = _i8_rows(fn, "q", q, W.in_dim, dev)
-    ps = _fast(qscale, F32, T, dev) or _arg(fn, "qscale", qscale, F32, T)
-    types, n = BF16_BITS if out_mode == OUT_BF16 else F32, T * W.out_dim
-    po = _fast(out, types, n, dev) or _arg(fn, "out", out, types, n)
-    err = None if err_word is None else _arg(fn, "err_word", err_word, I32, 1)
-    code = lib().moe_linear_i8(ctypes.byref(W), pq, ld, ps, T, po, out_mode, err, _stream(stream, dev))
-    if code:
-        _check(fn, code)
+    pq, ld, T = _i8_rows(fn, "q", q, W.in_dim)
+    ps = _arg(fn, "qscale", qscale, F32, T)
+    po = _arg(fn, "out", out, BF16_BITS if out_mode == OUT_BF16 else F32, T * W.out_dim)
+    err = _arg(fn, "err_word", err_word, I32, 1, optional=True)
+    _check(fn, lib().moe_linear_i8(ctypes.byref(W), pq, ld, ps, T, po, out_mode, err, _stream(stream)))
 
 
 class TieredPool:

@@ -2,11 +2,13 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
+BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_binding.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_RANGE = range(7)
 MOE_MAX_TOKENS = 524280  # most tokens one call takes
@@ -102,3 +104,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib
     return _lib
+
+
+_fast = None
+
+
+def binding():
+    """The extension that makes the calls of a few microseconds (``csrc/binding.cpp``), bound to libmoe.so.
+
+    Each of its functions returns the call's status, or None without having done anything where an argument does not
+    pass its checks.
+    """
+    global _fast
+    if _fast is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"_binding.so not built at {BINDING_PATH}; run int4_expert_ffn_top_b200.build.build()")
+        import torch  # noqa: F401  (the extension needs its libraries)
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        if not module.load(LIB_PATH):
+            raise RuntimeError(f"{BINDING_PATH} does not find its entry points in {LIB_PATH}")
+        _fast = module
+    return _fast

@@ -135,6 +135,17 @@ def test_product(cuda_ok, N, K, T, mode):
     check_linear(N, K, T, mode, bias=(N + T) % 2 == 0, pad=T % 3, seed=N + T)
 
 
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("N,K,T", [
+    (9000, 3000, 2), (9000, 40, 4), (5000, 100, 5), (70000, 64, 7),  # few tokens, many rows: no split of K, and little K
+    (40000, 144, 20), (65536, 100, 32),  # more tiles of 32 tokens than multiprocessors
+    (20001, 272, 50), (70000, 130, 33), (80001, 64, 20),  # CTA pairs, 64 tokens a tile, several tiles a pair
+    (4100, 1000, 450), (4099, 2050, 600), (4100, 144, 1000),  # 128, 192 and 256 tokens a tile, ragged last tiles
+    (4353, 130, 1025), (9001, 300, 2000), (4097, 4111, 513)])
+def test_product_of_many_tiles(cuda_ok, N, K, T, mode):
+    check_linear(N, K, T, mode, bias=(N + T) % 2 == 0, pad=T % 3, seed=N + T)
+
+
 @pytest.mark.parametrize("T", [1, 70, 130])
 def test_largest_sum_is_exact(cuda_ok, T):
     """All codes -128 over the longest rows: the largest magnitude a 32-bit sum has to hold."""
@@ -193,3 +204,58 @@ def test_quantised_projection_as_used(cuda_ok, T):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first)
+
+
+def test_call_that_waits_for_room_in_the_queue(cuda_ok):
+    """More calls than the device's queue holds, from two threads on their own streams: each waits without the
+    interpreter's lock, and both results hold."""
+    import threading
+    lin, W, sw, b = linear(512, 512, seed=3)
+    outs = []
+
+    def work(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            g = torch.Generator(device=DEV).manual_seed(k)
+            x = torch.randn((64, 512), device=DEV, generator=g)
+            q = torch.zeros((64, 512), dtype=torch.int8, device=DEV)
+            s = torch.empty(64, device=DEV)
+            out = torch.empty((64, 512), device=DEV)
+            for _ in range(1500):
+                M.moe_quant_i8(x, q, s)
+                M.moe_linear_i8(lin, q, s, out, M.OUT_F32)
+            torch.cuda.current_stream().synchronize()
+            outs.append((q, s, out))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    assert len(outs) == 2
+    for q, s, out in outs:
+        p, ref = product64(W, sw, b, q, s, 512)
+        assert ((out.double() - ref).abs() <= 3.01 * EPS32 * p.abs() + 1.01 * EPS32 * ref.abs()).all()
+
+
+def test_refusals_on_the_device(cuda_ok):
+    """What the quick way does not take is named by the full checks, and nothing is written."""
+    lin, *_ = linear(64, 64)
+    q, s, out = torch.zeros((4, 64), dtype=torch.int8, device=DEV), torch.zeros(4, device=DEV), torch.full((4, 64), 3.0, device=DEV)
+    for args, what in (((q[:, :32], s, out), "contiguous|rows hold"), ((q, s[:3], out), "qscale holds 3"),
+                       ((q, s, out[:3]), "out holds"), ((q, s.double(), out), "dtype"), ((q, s, out.half()), "dtype"),
+                       ((q.cpu(), s, out), "CUDA tensor"), ((q[0], s, out), r"\[T, ld\]"), ((q, s, out.T), "contiguous")):
+        with pytest.raises(ValueError, match=what):
+            M.moe_linear_i8(lin, *args, M.OUT_F32)
+    with pytest.raises(M.MoEError):
+        M.moe_linear_i8(lin, q, s, out, 5)
+    with pytest.raises(M.MoEError):
+        M.moe_linear_i8(lin, q.view(-1)[8:200].view(3, 64), s, out, M.OUT_F32)
+    with pytest.raises(TypeError):
+        M.moe_linear_i8(lin, q, [0.0], out, M.OUT_F32)
+    x = torch.zeros((4, 64), device=DEV)
+    for args, what in (((x.T, q, s), "contiguous"), ((x, q[:3], s), "q has 3 rows"), ((x.double(), q, s), "dtype"),
+                       ((x, q, s[:2]), "scale holds 2")):
+        with pytest.raises(ValueError, match=what):
+            M.moe_quant_i8(*args)
+    torch.cuda.synchronize()
+    assert (out == 3.0).all()

@@ -100,3 +100,19 @@ def test_binding_order_and_checks(rec):  # noqa: F811
         with pytest.raises((ValueError, TypeError)):
             call()
     assert len(rec.calls) == n
+
+
+def test_quick_way_takes_nothing_it_has_not_checked(lib):
+    """The extension answers None, without a call, to anything but tensors on the current CUDA device."""
+    b = _lib.binding()
+    x, q, s = torch.zeros((2, 64)), torch.zeros((2, 64), dtype=torch.int8), torch.zeros(2)
+    W = ctypes.addressof(_lib.moe_linear8(None, 64, None, None, 8, 64))
+    assert b.quant(x, q, s, None) is None and b.quant(x, q, s, float("nan")) is None and b.quant(x, q, s, "1") is None
+    assert b.quant(x, q, s) is None and b.quant(None, None, None, None) is None
+    assert b.linear(W, 0, q, s, x, 0, None) is None and b.linear(0, 0, q, s, x, 0, None) is None
+    assert b.linear(W, None, q, s, x, 0, None) is None and b.linear("w", 0, q, s, x, 0, None) is None
+    L = _lib.moe_layer()
+    A = ctypes.addressof(L)
+    assert b.layer(A, x, None, 1e-6, 2, None, None, q, s, x, 0, q, None) is None
+    assert b.layer(A, None, x, 1e-6, 99, None, None, q, s, x, 0, q, None) is None
+    assert b.layer(A, None, x, "eps", 2, None, None, q, s, x, 0, q, None) is None

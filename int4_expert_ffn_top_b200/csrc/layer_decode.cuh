@@ -22,6 +22,14 @@
 // by a power of two that puts its largest entry in [2^9, 2^10); hidden values h are
 // stored as two fp16 numbers, hi and 2^11 (h - hi), 22 bits together, in two columns
 // of the N side.  Products are exact, group sums and everything after are fp32.
+//
+// What bounds it (B200, 35B shape).  One token, 20.5 us: the chain of steps; 9.7 MB of weights take 1.5 us, five
+// barriers and hand-overs 1.1 us and more each, the top-K 3, gate/up 3.7, down 3.  16 tokens, 49 us (103 MB, 16 us at
+// copy speed), and 32, 90 us: the instructions around the MMAs.  Eight codes take five half-rate integer operations and
+// two MMAs of which one to three of eight columns are used; the integer pipe is busy 41 % of the time, issue 44 %, shared
+// memory and L1 33 %, DRAM a third.  No single one of them gives way: bringing the weights to L2 ahead of time, the
+// columns to L1 or registers, leaving the unused columns' loads out, or dropping the decoding altogether moves the down
+// loop by less than a tenth each.  16 warps: 8, 12, 20 and 24 take 62, 55, 54 and 55 us for 16 tokens.
 #pragma once
 
 #include "common.cuh"
@@ -241,8 +249,9 @@ struct Raw8<false> {
 };
 
 // Token t's image by `warps` warps (this one is number wi): u scaled by a power of two c, fp16, pair order, odd pairs
-// / 16; per group 2^-24 sum of c u; 1/c.  The squares are summed with their rounding errors (two fp32 numbers per lane), then in 64 bits: fp64 runs at a few lanes a
-// cycle, and a token's 2,048 squares in it cost more than the rest of the image.
+// / 16; per group 2^-24 sum of c u; 1/c.  The squares are summed with their rounding errors (two fp32 numbers per lane),
+// then in 64 bits: fp64 runs at a few lanes a cycle, and a token's 2,048 squares in it cost more than the rest of the
+// image.
 template <bool F32>
 __device__ __noinline__ void build_image(const Args& a, int t, int wi, int warps, int team, double* red, uint8_t* row,
                                          float* us, float* ic, bool write_u) {
@@ -376,10 +385,10 @@ __device__ __noinline__ void build_image(const Args& a, int t, int wi, int warps
 // ----------------------------------------------------------------------------- int4 units
 // The unit of weight traffic and of work: the codes of 16 rows x 4 groups (2 where a row has only 2), brought by one
 // warp into its own buffers with cp.async and used by that warp alone: no barrier is needed between copy and use, and
-// each of 24 warps has two units of 2 KB, one in use and one in flight (a third takes L1 away from the token images:
-// 62 us against 57 for 16 tokens of the 35B shape).  16-byte chunk c of row m lies at place c ^ 2 (m % 4) of the row's 128 bytes, so that the 8-byte fragment reads of 4 rows fall on different banks.  The
-// scales and biases come for two units at a time (16 bytes each of a row) into sets of their own, [16 rows][scales,
-// biases].
+// each warp has two units of 2 KB, one in use and one in flight (a third takes L1 away from the token images: 62 us
+// against 57 for 16 tokens of the 35B shape, when there were 24 warps).  16-byte chunk c of row m lies at place
+// c ^ 2 (m % 4) of the row's 128 bytes, so that the 8-byte fragment reads of 4 rows fall on different banks.  The scales
+// and biases come for two units at a time (16 bytes each of a row) into sets of their own, [16 rows][scales, biases].
 // Row m of a unit is record (m % 8) * step_lo + (m / 8) * step_hi: gate rows over up rows for gate/up (2, 1), rows in
 // order for down (1, 8).
 struct UnitPlan {  // a lane's places: bytes from the unit's first record (its chunk of row lane/8; its scales)
@@ -546,7 +555,7 @@ __device__ __noinline__ float dot_r(const uint16_t* B, const float* t, int r) {
 #pragma unroll 2
   for (int i = 0; i < r; i += 8) {
     const uint4 b = __ldg(reinterpret_cast<const uint4*>(B + i));
-    const float4 p = __ldcg(reinterpret_cast<const float4*>(t + i)), q = __ldcg(reinterpret_cast<const float4*>(t + i + 4));
+    const float4 p = *reinterpret_cast<const float4*>(t + i), q = *reinterpret_cast<const float4*>(t + i + 4);
     v = fmaf(lo_half(b.x), p.x, v);
     v = fmaf(hi_half(b.x), p.y, v);
     v = fmaf(lo_half(b.y), p.z, v);
@@ -1130,26 +1139,46 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   const size_t hrow = static_cast<size_t>(a.I) * 2;  // bytes of one hi or lo row
   const int logm = r > 16 ? 1 : 0;  // 16-row tiles of A: 1 or 2
   float* td = reinterpret_cast<float*>(sm + S.td);
-  // LoRA A on hidden values: routed, each (block of slots, 16 rows of A) once in the grid; shared, in every CTA, with
-  // the groups split over as many warps as there are (partial sums [part][token][kMaxR])
+  // LoRA A on hidden values: routed, each (block of slots, 16 rows of A) once in the grid, its groups split over eight
+  // warps of a CTA and joined there (a warp for the whole task waits for its loads several times over: 94 us against 88
+  // for 32 tokens of the 35B shape); shared, in every CTA, with the groups split over as many warps as there are
+  // (partial sums [part][token][kMaxR])
   int logp = 0;
   while (logp < 3 && (sh_blocks << logm) << (logp + 1) <= kWarps && G2 >> (logp + 1) > 0) ++logp;
 #pragma unroll 1
   for (int kind = 0; kind < 2; ++kind) {
     const uint16_t* A = kind ? a.shA[2] : a.exA;
     if (!A) continue;
-    const int tasks = (kind ? sh_blocks << logp : nel - sh_blocks) << logm;
+    const int lp = kind ? logp : min(a.logI - 6, 3), mask = (1 << lp) - 1;
+    const int tasks = (kind ? sh_blocks : nel - sh_blocks) << logm;
+    const int w0 = kind ? kWarps - 1 - warp : warp, step = (kind ? 1 : grid) * (kWarps >> lp);
 #pragma unroll 1
-    for (int q = kind ? kWarps - 1 - warp : cta + grid * warp; q < tasks; q += kind ? kWarps : grid * kWarps) {
-      const int m0 = (q & ((1 << logm) - 1)) * 16, part = kind ? (q >> logm) & ((1 << logp) - 1) : 0;
-      const int ei = kind ? q >> (logm + logp) : q >> logm, el = els[(kind ? 0 : sh_blocks) + ei];
+    for (int q0 = kind ? 0 : cta; q0 < tasks; q0 += step) {  // the same turns in every warp
+      const int q = q0 + (kind ? 1 : grid) * (w0 >> lp), part = w0 & mask;
+      const bool on = q < tasks;
+      const int m0 = (q & ((1 << logm) - 1)) * 16, el = on ? els[(kind ? 0 : sh_blocks) + (q >> logm)] : 1 << 20;
       const int d = el & 511, s0 = (el >> 9) & 511, n = el >> 20, cs = s0 + min(g >> 1, n - 1);
-      const uint16_t* M = A + (kind ? 0 : static_cast<size_t>(dist[d]) * r * a.I);
-      const int pos = kind ? TK + cs : slots[cs] & 0xffff, span = kind ? G2 >> logp : G2;
       float v[4];
-      f16_rows(M + static_cast<size_t>(min(m0 + g, r - 1)) * a.I, M + static_cast<size_t>(min(m0 + g + 8, r - 1)) * a.I,
-                     part * span, (part + 1) * span, hb + (static_cast<size_t>(pos) * 2 + (g & 1)) * hrow, v);
-      if (tig < n) {
+      if (on) {
+        const uint16_t* M = A + (kind ? 0 : static_cast<size_t>(dist[d]) * r * a.I);
+        const int pos = kind ? TK + cs : slots[cs] & 0xffff, span = G2 >> lp;
+        f16_rows(M + static_cast<size_t>(min(m0 + g, r - 1)) * a.I, M + static_cast<size_t>(min(m0 + g + 8, r - 1)) * a.I,
+                 part * span, (part + 1) * span, hb + (static_cast<size_t>(pos) * 2 + (g & 1)) * hrow, v);
+      }
+      if (kind == 0) {  // join the parts
+        float4* sums = reinterpret_cast<float4*>(scratch);
+        if (on && part > 0) sums[warp * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+        named_sync(15, kThreads);
+        if (on && part == 0) {
+#pragma unroll 1
+          for (int w = 1; w <= mask; ++w) {
+            const float4 p = sums[(warp + w) * 32 + lane];
+            v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+          }
+        }
+        named_sync(15, kThreads);
+      }
+      if (on && tig < n && (kind || part == 0)) {
         float* o = kind ? td + (part * T + s0 + tig) * kMaxR : a.tex + static_cast<size_t>(slots[s0 + tig] & 0xffff) * r;
         if (m0 + g < r) o[m0 + g] = fmaf(v[1], 0x1p-11f, v[0]);
         if (m0 + g + 8 < r) o[m0 + g + 8] = fmaf(v[3], 0x1p-11f, v[2]);
@@ -1198,10 +1227,13 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
       if (lane < ndr)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(a.exB + (static_cast<size_t>(sel[s]) * a.H + dr0 + lane) * r));
   }
-  if (a.exA)
+  if (a.exA) {
     grid_wait(a.bar, B_EXDOWN, true, failed, a.err, a.timeout_ns);
-  else
+    for (int i = tid; i < TK * r / 32; i += kThreads)  // every row of a slot reads its A h
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.tex + 32 * i));
+  } else {
     named_sync(15, kThreads);
+  }
 
   // --------------------------------------------------------------------------- combine
   if (a.shA[2] && logp > 0) {  // the parts of the shared down adapter's A h

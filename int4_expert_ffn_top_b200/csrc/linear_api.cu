@@ -211,13 +211,25 @@ moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, con
   int dev = 0;
   const int nsm = multiprocessors(&dev), in = W->in_dim;
   if (nsm < 1) return MOE_ERR_CUDA;
-  if (T == 1) return launch_rows<4, 1>(a, nsm, st);
-  if (T == 2) return launch_rows<4, 2>(a, nsm, st);
-  if (T <= 4) return launch_rows<4, 4>(a, nsm, st);
-  if (T <= 8) return launch_rows<2, 8>(a, nsm, st);
+  // Few tokens: dp4a over the weight rows where that is done before a tensor-core kernel has begun (2^24 products take
+  // it 4 us; the cluster split takes 5 for anything small: 3 x 1,008 -> 2,051 2.6 against 5.0 us, but 3 x 2,048 -> 4,096
+  // 8.1 against 5.8 and 8 x 2,048 -> 65,536 65 against 29), and for one or two tokens with rows long enough to keep a
+  // warp's loads going (2,048 -> 65,536: 21.7 against 28.5 us, two tokens 25.6 against 28.6; short rows, 512 -> 200,000:
+  // 39.9 against 30.4, two tokens 1,024 -> 131,072: 35.2 against 29.7).
+  if (T <= 8) {
+    const int nt = T <= 2 ? T : T <= 4 ? 4 : 8;
+    if (static_cast<long long>(a.N) * a.K16 * nt <= 1 << 20 || (T <= 2 && a.K16 >= 64 * T)) {
+      if (nt == 1) return launch_rows<4, 1>(a, nsm, st);
+      if (nt == 2) return launch_rows<4, 2>(a, nsm, st);
+      if (nt == 4) return launch_rows<4, 4>(a, nsm, st);
+      return launch_rows<2, 8>(a, nsm, st);
+    }
+  }
   const long long m = (a.N + l8::kGM - 1) / l8::kGM, m2 = (m + 1) / 2;
   auto tiles = [&](long long rows, int bn) { return rows * ((T + bn - 1) / bn); };
-  if (tiles(m, 32) <= nsm || (T <= 32 && tiles(m, 32) <= 4 * nsm)) return launch_split<32>(a, in, err_word, nsm, dev, st);
+  // K split over clusters while the tiles find a multiprocessor each; for up to 16 tokens, two (16 x 2,048 -> 30,000:
+  // 16.5 us against 16.9 with CTA pairs; 32 tokens 18.4 against 16.7, 16 x 2,048 -> 65,536 31.4 against 29.4)
+  if (tiles(m, 32) <= nsm || (T <= 16 && m <= 2 * nsm)) return launch_split<32>(a, in, err_word, nsm, dev, st);
   if (tiles(m, 64) <= nsm) return launch_split<64>(a, in, err_word, nsm, dev, st);
   // the token tile whose waves of tiles take the least time: a tile costs its columns, and 16 more for its turn
   auto cost = [&](int bn) { return (tiles(m2, bn) + nsm / 2 - 1) / (nsm / 2) * (bn + 16); };

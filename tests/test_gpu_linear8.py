@@ -138,7 +138,8 @@ def test_product(cuda_ok, N, K, T, mode):
 @pytest.mark.parametrize("mode", [0, 1, 2])
 @pytest.mark.parametrize("N,K,T", [
     (9000, 3000, 2), (9000, 40, 4), (5000, 100, 5), (70000, 64, 7),  # few tokens, many rows: no split of K, and little K
-    (40000, 144, 20), (65536, 100, 32),  # more tiles of 32 tokens than multiprocessors
+    (200000, 512, 1), (131072, 1000, 2), (4096, 2048, 3), (2051, 1008, 8),  # both sides of the few-token rule
+    (30000, 333, 16), (40000, 144, 20), (65536, 100, 32),  # more tiles of 32 tokens than multiprocessors
     (20001, 272, 50), (70000, 130, 33), (80001, 64, 20),  # CTA pairs, 64 tokens a tile, several tiles a pair
     (4100, 1000, 450), (4099, 2050, 600), (4100, 144, 1000),  # 128, 192 and 256 tokens a tile, ragged last tiles
     (4353, 130, 1025), (9001, 300, 2000), (4097, 4111, 513)])

@@ -136,9 +136,33 @@ __global__ void __launch_bounds__(kQThreads) quant_kernel(const QuantArgs a) {
     p.load(a.x, row + static_cast<size_t>(i) * P::kN);
     put(p, i);
   }
+  // squares that fp32 may not hold (the same in the whole block): summed of values scaled by a power of two that keeps the
+  // largest's square, times 65,536, in range
+  const bool far = a.eps >= 0.f && !zero && (m > 1e16f || m < 1e-15f);
+  if (far) {
+    const float sc = m > 1.f ? 0x1p-96f : 0x1p96f;
+    ss = 0.f;
+#pragma unroll 1
+    for (int i = tid; i < a.H; i += kStep) {
+      Piece<BF16, false> p;
+      p.load(a.x, row + i);
+      ss = fmaf(p.v[0] * sc, p.v[0] * sc, ss);
+    }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    __syncthreads();
+    if ((tid & 31) == 0) red[1][tid >> 5] = ss;
+    __syncthreads();
+    ss = 0.f;
+#pragma unroll 1
+    for (int w = 0; w < kQThreads / 32; ++w) ss += red[1][w];
+  }
   if (tid == 0) {
     float s = m / 127.f;
-    if (a.eps >= 0.f && m > 0.f) s = m * (1.f / sqrtf(ss / static_cast<float>(a.H) + a.eps)) / 127.f;
+    if (far)
+      s = static_cast<float>(m / sqrt(static_cast<double>(ss) / a.H * (m > 1.f ? 0x1p192 : 0x1p-192) + a.eps) / 127.0);
+    else if (a.eps >= 0.f && m > 0.f)
+      s = m * (1.f / sqrtf(ss / static_cast<float>(a.H) + a.eps)) / 127.f;
     a.scale[t] = fine ? s : __uint_as_float(0x7fc00000u);
   }
 }

@@ -113,6 +113,22 @@ def test_extreme_magnitudes(cuda_ok, scale):
     assert ((s.double() - m / 127).abs() <= EPS32 * 1.01 * m / 127 + 2.0 ** -150).all()
 
 
+@pytest.mark.parametrize("H", [104, 2000, 65536])
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 1e-25, 1e-16, 1e15, 1e17, 1e20, 1e30, 3e38])
+def test_norm_of_extreme_magnitudes(cuda_ok, scale, H):
+    """Rows whose squares overflow or vanish in fp32: the scale still holds."""
+    g = torch.Generator(device=DEV).manual_seed(H)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = ((torch.rand((3, H), device=DEV, generator=g) * 2 - 1) * scale).to(dtype)
+        for eps in (0.0, 1e-6):
+            q, s = quant(x, eps)
+            ref, m = codes_of(x)
+            assert torch.equal(q[:, :H].double(), ref)
+            want = torch.where(m > 0, m / (x.double().square().mean(1) + eps).sqrt() / 127, 0.0)
+            tol = (0.5 * (H / 256 + 16) + 6) * 1.01 * EPS32
+            assert ((s.double() - want).abs() <= tol * want + 2.0 ** -149).all()
+
+
 def test_zero_and_non_finite_rows(cuda_ok):
     x = torch.randn((6, 70), device=DEV)
     x[0] = 0
@@ -260,3 +276,19 @@ def test_refusals_on_the_device(cuda_ok):
             M.moe_quant_i8(*args)
     torch.cuda.synchronize()
     assert (out == 3.0).all()
+
+
+def test_outputs_past_32_bit_offsets(cuda_ok):
+    """More than 2^32 output elements: the last tokens and the last columns land where they belong."""
+    N, K, T = 66000, 48, 65100
+    lin, W, sw, b = linear(N, K, seed=9)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    q = torch.randint(-128, 128, (T, K), dtype=torch.int8, device=DEV, generator=g)
+    sx = torch.rand(T, device=DEV, generator=g) * 0.1
+    out = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+    M.moe_linear_i8(lin, q, sx, out, M.OUT_BF16)
+    for rows in (slice(0, 40), slice(32500, 32600), slice(T - 300, T)):
+        p, ref = product64(W, sw, b, q[rows], sx[rows], K)
+        tol = 3.01 * EPS32 * p.abs() + (1.01 * EPS32 + 1.01 * EPSBF) * ref.abs()
+        assert ((out[rows].double() - ref).abs() <= tol).all()
+    assert not torch.isnan(out[::997]).any()

@@ -223,7 +223,7 @@ size_t moe_workspace_size(const moe_layer* L, int32_t T, int32_t K);
  *   64 bits) and then to bf16.
  * exec_idx [T][K] int32 or NULL: experts to execute in place of the router's own
  *   top-K (predicted routing); a value outside [0,E) is clamped to 0 or E-1,
- *   and an expert listed twice counts twice.
+ *   and an expert listed twice counts twice.  It may not overlap idx.
  * logits [T][E] fp32 or NULL; idx [T][K] int32 (the router's own top-K, ordering
  *   and ties as moe_route_topk; a NaN logit ranks below every number) and w [T][K]
  *   fp32 are required outputs.

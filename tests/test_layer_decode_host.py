@@ -53,6 +53,17 @@ def test_refusals(lib):
         assert call(lib, layer(**kw)) == uns, kw
 
 
+def test_given_experts_apart_from_the_routers(lib):
+    """exec_idx is read by every CTA after idx is written by one: the two may not overlap."""
+    L = layer()
+    for at in (A, A + 4, A + 28, A - 28):
+        assert lib.moe_layer_decode(ctypes.byref(L), A, None, 0.0, 2, 4, at, None, A, A, A, 0, A, 1 << 30, None,
+                                    None) == _lib.MOE_ERR_INVALID_ARG
+    for at in (A + 32, A - 32):  # as far as the workspace check
+        assert lib.moe_layer_decode(ctypes.byref(L), A, None, 0.0, 2, 4, at, None, A, A, A, 0, A, 16, None,
+                                    None) == _lib.MOE_ERR_WORKSPACE
+
+
 def test_workspace_size(lib):
     size = lambda t, k=4, **kw: lib.moe_layer_decode_workspace_size(ctypes.byref(layer(**kw)), t, k)  # noqa: E731
     assert lib.moe_layer_decode_workspace_size(None, 1, 4) == 0 and size(-1) == size(33) == size(1, 0) == 0

@@ -12,11 +12,19 @@
 // tokens (or slots) of an expert as N: an expert has one to a few of them, so N = 8
 // is what there is, and the fp16 operand comes straight out of the packed codes in
 // registers.  fp16 numbers with a zero exponent field are m 2^-24, so a masked
-// nibble IS the code times 2^-24, exactly, without a conversion: bits 0..3 of each
-// half after (w & 0x000F000F), and 16 times the code after (w & 0x00F000F0), which
-// the other operand makes up for (its entries for k % 4 odd are stored / 16).  A
-// word's four half pairs are (q_j, q_{j+4}), "pair order", and the other operand is
-// stored in the same order.
+// nibble IS the code times a power of two, exactly, without a conversion: times
+// 2^-22 in bits 2..5 of each half, times 2^-18 in bits 6..9.  A word's four half
+// pairs are (q_j, q_{j+4}), "pair order", and the other operand is stored in the
+// same order.
+//
+// Where in the mantissa matters: the MMA aligns its products by their exponents and
+// a subnormal counts with the smallest one, so a code's leading zeros are bits lost at
+// the other end of the sum.  Gate/up takes a word's even pairs at 2^-22 and its odd
+// ones at 2^-18 (two shifts and four masks for 8 codes; the images' odd pairs are stored
+// / 16); down, whose columns have 11 bits and not 8, takes all four at 2^-18 (four
+// shifts).  Gate/up at 2^-24 and 2^-20 (one shift) and down as gate/up is now leave the
+// layer's output off by 6e-7 to 1.1e-6 of its size instead of 3e-7 to 6e-7, and are 0 to
+// 3 % faster (35B shape, 1 / 16 / 32 tokens in a graph: 21.9 / 51.3 / 93 us, 22.2 / 51.8 / 94).
 //
 // Precision.  u (bf16, 8 significant bits) is exact in fp16 after scaling each token
 // by a power of two that puts its largest entry in [2^9, 2^10); hidden values h are
@@ -25,8 +33,8 @@
 //
 // What bounds it (B200, 35B shape).  One token, 20.5 us: the chain of steps; 9.7 MB of weights take 1.5 us, five
 // barriers and hand-overs 1.1 us and more each, the top-K 3, gate/up 3.7, down 3.  16 tokens, 49 us (103 MB, 16 us at
-// copy speed), and 32, 88 us: the instructions around the MMAs.  Eight codes take five half-rate integer operations and
-// two MMAs of which one to three of eight columns are used; the integer pipe is busy 41 % of the time, issue 44 %, shared
+// copy speed), and 32, 88 us: the instructions around the MMAs.  Eight codes take six to eight half-rate integer operations
+// and two MMAs of which one to three of eight columns are used; the integer pipe is busy 41 % of the time, issue 44 %, shared
 // memory and L1 33 %, DRAM a third.  No single one of them gives way: bringing the weights to L2 ahead of time, the
 // columns to L1 or registers, leaving the unused columns' loads out, or dropping the decoding altogether moves the down
 // loop by less than a tenth each.  16 warps: 8, 12, 20 and 24 take 62, 55, 54 and 55 us for 16 tokens.
@@ -449,15 +457,15 @@ MOE_DEV Frag load_frag(const uint8_t* col, int i) {
   return {p[0], p[1]};
 }
 
-// acc += one unit of gate/up rows times 8 columns, two groups at a time (four would take half as many warps again in
-// registers).
+// acc += 2^-22 of one unit of gate/up rows times 8 columns (ua, ub: 2^-24 of the groups' sums), two groups at a time (four
+// would take half as many warps again in registers).
 MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* set, int half, const uint8_t* col, const float* ua, const float* ub,
                           float (&acc)[4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   // chunk 2 i + tig / 2 of row g (and g + 8)
   const uint8_t* ra = buf + g * 128 + 8 * (tig & 1);
   const int ch = (tig >> 1) ^ 2 * (g & 3);
-  const uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
+  const uint32_t lo = 0x003C003Cu, hi = 0x03C003C0u;
   const uint8_t* sp = set + 2 * half * g;
   const uint2 sa2 = *reinterpret_cast<const uint2*>(sp), ba2 = *reinterpret_cast<const uint2*>(sp + half);
   const uint2 sb2 = *reinterpret_cast<const uint2*>(sp + 16 * half), bb2 = *reinterpret_cast<const uint2*>(sp + 17 * half);
@@ -469,18 +477,19 @@ MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* set, int half, cons
       const Frag f = load_frag(col, 2 * h + i);
       const uint8_t* w = ra + 16 * (ch ^ (4 * h + 2 * i));
       const uint2 wa = *reinterpret_cast<const uint2*>(w), wb = *reinterpret_cast<const uint2*>(w + 1024);
-      const uint32_t wa8 = wa.x >> 8, wb8 = wb.x >> 8, va8 = wa.y >> 8, vb8 = wb.y >> 8;
-      mma16_0(d[i], wa.x & lo, wb.x & lo, wa.x & hi, wb.x & hi, f.x.x, f.x.y);
-      mma16(d[i], wa8 & lo, wb8 & lo, wa8 & hi, wb8 & hi, f.x.z, f.x.w);
-      mma16(d[i], wa.y & lo, wb.y & lo, wa.y & hi, wb.y & hi, f.y.x, f.y.y);
-      mma16(d[i], va8 & lo, vb8 & lo, va8 & hi, vb8 & hi, f.y.z, f.y.w);
+      const uint32_t p0 = wa.x << 2, p1 = wa.x >> 6, p2 = wa.y << 2, p3 = wa.y >> 6;
+      const uint32_t q0 = wb.x << 2, q1 = wb.x >> 6, q2 = wb.y << 2, q3 = wb.y >> 6;
+      mma16_0(d[i], p0 & lo, q0 & lo, p0 & hi, q0 & hi, f.x.x, f.x.y);
+      mma16(d[i], p1 & lo, q1 & lo, p1 & hi, q1 & hi, f.x.z, f.x.w);
+      mma16(d[i], p2 & lo, q2 & lo, p2 & hi, q2 & hi, f.y.x, f.y.y);
+      mma16(d[i], p3 & lo, q3 & lo, p3 & hi, q3 & hi, f.y.z, f.y.w);
     }
     const uint32_t s0 = h ? sa2.y : sa2.x, b0 = h ? ba2.y : ba2.x, s1 = h ? sb2.y : sb2.x, b1 = h ? bb2.y : bb2.x;
     const float2 u = *reinterpret_cast<const float2*>(ua + 2 * h), v = *reinterpret_cast<const float2*>(ub + 2 * h);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float p = i ? hi_half(s0) : lo_half(s0), q = i ? hi_half(b0) : lo_half(b0);
-      const float r = i ? hi_half(s1) : lo_half(s1), t = i ? hi_half(b1) : lo_half(b1), ui = i ? u.y : u.x, vi = i ? v.y : v.x;
+      const float r = i ? hi_half(s1) : lo_half(s1), t = i ? hi_half(b1) : lo_half(b1), ui = 4.f * (i ? u.y : u.x), vi = 4.f * (i ? v.y : v.x);
       acc[0] = fmaf(q, ui, fmaf(p, d[i][0], acc[0]));
       acc[1] = fmaf(q, vi, fmaf(p, d[i][1], acc[1]));
       acc[2] = fmaf(t, ui, fmaf(r, d[i][2], acc[2]));
@@ -491,15 +500,12 @@ MOE_DEV void gate_up_unit(const uint8_t* buf, const uint8_t* set, int half, cons
 
 // acc += one unit of down rows (15 of them; row 15 holds code 15 everywhere: 15 times the columns' sums) times the 8
 // columns (hi and lo of 4 slots).
-// Codes enter as code 2^-22 (and 16 times that).  The MMA aligns its products by their exponents, and a subnormal
-// counts with the smallest one, so two more of the mantissa's bits in use keep two more of h's 11 in the sum (u's 8 fit
-// either way): the result is off by 7e-7 of its size instead of 3e-6.
 MOE_DEV void down_unit(const uint8_t* buf, const uint8_t* set, int half, Frag f0, Frag f1, const uint8_t* col, bool whole,
                        float (&acc)[4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   const uint8_t* ra = buf + g * 128 + 8 * (tig & 1);
   const int ch = (tig >> 1) ^ 2 * (g & 3);
-  const uint32_t lo = 0x003C003Cu, hi = 0x03C003C0u;
+  const uint32_t top = 0x03C003C0u;
   Frag f2 = f0, f3 = f1;
   if (whole) f2 = load_frag(col, 2), f3 = load_frag(col, 3);
   const uint8_t *sp = set + 2 * half * g, *sq = sp + 16 * half;
@@ -514,12 +520,16 @@ MOE_DEV void down_unit(const uint8_t* buf, const uint8_t* set, int half, Frag f0
       const Frag& f = h ? (i ? f3 : f2) : (i ? f1 : f0);
       const uint8_t* w = ra + 16 * (ch ^ (4 * h + 2 * i));
       const uint2 wa = *reinterpret_cast<const uint2*>(w), wb = *reinterpret_cast<const uint2*>(w + 1024);
-      const uint32_t p0 = wa.x << 2, p1 = wa.x >> 6, p2 = wa.y << 2, p3 = wa.y >> 6;
-      const uint32_t q0 = wb.x << 2, q1 = wb.x >> 6, q2 = wb.y << 2, q3 = wb.y >> 6;
-      mma16_0(d[i], p0 & lo, q0 & lo, p0 & hi, q0 & hi, f.x.x, f.x.y);
-      mma16(d[i], p1 & lo, q1 & lo, p1 & hi, q1 & hi, f.x.z, f.x.w);
-      mma16(d[i], p2 & lo, q2 & lo, p2 & hi, q2 & hi, f.y.x, f.y.y);
-      mma16(d[i], p3 & lo, q3 & lo, p3 & hi, q3 & hi, f.y.z, f.y.w);
+      auto four = [&](float (&o)[4], bool first, uint32_t x, uint32_t y, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+        const uint32_t a0 = (x << 6) & top, a1 = (y << 6) & top, a2 = (x << 2) & top, a3 = (y << 2) & top;
+        if (first)
+          mma16_0(o, a0, a1, a2, a3, b0, b1);
+        else
+          mma16(o, a0, a1, a2, a3, b0, b1);
+        mma16(o, (x >> 2) & top, (y >> 2) & top, (x >> 6) & top, (y >> 6) & top, b2, b3);
+      };
+      four(d[i], true, wa.x, wb.x, f.x.x, f.x.y, f.x.z, f.x.w);
+      four(d[i], false, wa.y, wb.y, f.y.x, f.y.y, f.y.z, f.y.w);
     }
     const uint32_t s0 = h ? sa2.y : sa2.x, b0 = h ? ba2.y : ba2.x, s1 = h ? sb2.y : sb2.x, b1 = h ? bb2.y : bb2.x;
 #pragma unroll
@@ -541,9 +551,8 @@ MOE_DEV void down_unit(const uint8_t* buf, const uint8_t* set, int half, Frag f0
 MOE_DEV void store_h(const Args& a, int row, int j, float x, float y) {
   const float v = silu(x) * y;
   if (fabsf(v) > kF16Max && fabsf(v) <= 3.402823466e38f) report(a.err, 6 /* MOE_ERR_RANGE */);
-  const float s = (j & 1) ? v * 0.0625f : v;
-  const __half hi = __float2half_rn(s);
-  const __half lo = __float2half_rn((s - __half2float(hi)) * 2048.f);
+  const __half hi = __float2half_rn(v);
+  const __half lo = __float2half_rn((v - __half2float(hi)) * 2048.f);
   uint16_t* p = a.h + static_cast<size_t>(row) * 2 * a.I + pair_pos(j);
   p[0] = __half_as_ushort(hi);
   p[a.I] = __half_as_ushort(lo);
@@ -568,8 +577,9 @@ __device__ __noinline__ float dot_r(const uint16_t* B, const float* t, int r) {
   return v;
 }
 
-// Rows g and g + 8 of an fp16 matrix (row pointers) over groups [g0, g1) times 8 columns of image layout: ev + 16 od.
-MOE_DEV void f16_rows(const uint16_t* ra, const uint16_t* rb, int g0, int g1, const uint8_t* col, float (&v)[4]) {
+// Rows g and g + 8 of an fp16 matrix (row pointers) over groups [g0, g1) times 8 columns in pair order; what the odd
+// pairs of a column are stored divided by (images: 16, hidden values: 1).
+MOE_DEV void f16_rows(const uint16_t* ra, const uint16_t* rb, int g0, int g1, const uint8_t* col, float odd, float (&v)[4]) {
   const int tig = threadIdx.x & 3;
   float ev[4] = {0.f, 0.f, 0.f, 0.f}, od[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -585,7 +595,7 @@ MOE_DEV void f16_rows(const uint16_t* ra, const uint16_t* rb, int g0, int g1, co
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = fmaf(16.f, od[i], ev[i]);
+  for (int i = 0; i < 4; ++i) v[i] = fmaf(odd, od[i], ev[i]);
 }
 
 // ----------------------------------------------------------------------------- top-K and gating of one token (a warp)
@@ -790,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
         const int j = row - (a.E + 1);  // gate's rows, then up's
         const uint16_t* A = (a.shA[0] && j < r) ? a.shA[0] + static_cast<size_t>(j) * a.H
                                                 : a.shA[1] + static_cast<size_t>(a.shA[0] ? j - r : j) * a.H;
-        f16_rows(A, A, g0, g1, col, v);
+        f16_rows(A, A, g0, g1, col, 16.f, v);
       }
       if (g < n) *reinterpret_cast<float2*>(scratch + ((warp * 4 + b) * 8 + g) * 8 + 2 * tig) = make_float2(v[0], v[1]);
     }
@@ -849,8 +859,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
       const int t = 8 * warp + 2 * tig, pr = 8 * ti + g;
       if (pr < nsp) {
         float2* o = reinterpret_cast<float2*>(sraw) + pr;
-        if (t < T) o[t * 16] = make_float2(v.x * 0x1p24f * ic[t], v.z * 0x1p24f * ic[t]);
-        if (t + 1 < T) o[(t + 1) * 16] = make_float2(v.y * 0x1p24f * ic[t + 1], v.w * 0x1p24f * ic[t + 1]);
+        if (t < T) o[t * 16] = make_float2(v.x * 0x1p22f * ic[t], v.z * 0x1p22f * ic[t]);
+        if (t + 1 < T) o[(t + 1) * 16] = make_float2(v.y * 0x1p22f * ic[t + 1], v.w * 0x1p22f * ic[t + 1]);
       }
     }
     named_sync(15, kThreads);
@@ -1033,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
 #pragma unroll 1
       for (int q = q0; q < q1; ++q) {
         const int sl = slots[q] & 0xffff;
-        const float k = ic[slots[q] >> 16] * 0x1p24f;
+        const float k = ic[slots[q] >> 16] * 0x1p22f;
         float x = (q > q0 ? acc[1] : acc[0]) * k, y = (q > q0 ? acc[3] : acc[2]) * k;
         if (a.exAgu) {
           const uint16_t* B = a.exBgu + (static_cast<size_t>(dist[d]) * 2 * a.I + 2 * j) * r;
@@ -1163,7 +1173,7 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
         const uint16_t* M = A + (kind ? 0 : static_cast<size_t>(dist[d]) * r * a.I);
         const int pos = kind ? TK + cs : slots[cs] & 0xffff, span = G2 >> lp;
         f16_rows(M + static_cast<size_t>(min(m0 + g, r - 1)) * a.I, M + static_cast<size_t>(min(m0 + g + 8, r - 1)) * a.I,
-                 part * span, (part + 1) * span, hb + (static_cast<size_t>(pos) * 2 + (g & 1)) * hrow, v);
+                 part * span, (part + 1) * span, hb + (static_cast<size_t>(pos) * 2 + (g & 1)) * hrow, 1.f, v);
       }
       if (kind == 0) {  // join the parts
         float4* sums = reinterpret_cast<float4*>(scratch);
@@ -1214,8 +1224,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
       if (tig < n) {
         const int p = sh ? TK + s0 + tig : slots[s0 + tig] & 0xffff;
         float* y = scratch + (wi * NS + p) * RS + (ei < nel ? 0 : 16);
-        y[g] = fmaf(acc[1], 0x1p-11f, acc[0]) * 0x1p22f;
-        if (g < 7) y[g + 8] = fmaf(acc[3], 0x1p-11f, acc[2]) * 0x1p22f;
+        y[g] = fmaf(acc[1], 0x1p-11f, acc[0]) * 0x1p18f;
+        if (g < 7) y[g + 8] = fmaf(acc[3], 0x1p-11f, acc[2]) * 0x1p18f;
       }
       ei = ne;
       base = after;

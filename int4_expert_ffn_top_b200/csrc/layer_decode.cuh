@@ -31,9 +31,9 @@
 // stored as two fp16 numbers, hi and 2^11 (h - hi), 22 bits together, in two columns
 // of the N side.  Products are exact, group sums and everything after are fp32.
 //
-// What bounds it (B200, 35B shape).  One token, 20.5 us: the chain of steps; 9.7 MB of weights take 1.5 us, five
-// barriers and hand-overs 1.1 us and more each, the top-K 3, gate/up 3.7, down 3.  16 tokens, 49 us (103 MB, 16 us at
-// copy speed), and 32, 88 us: the instructions around the MMAs.  Eight codes take six to eight half-rate integer operations
+// What bounds it (B200, 35B shape).  One token, 22 us: the chain of steps; 9.7 MB of weights take 1.5 us, five
+// barriers and hand-overs 1.1 us and more each, the top-K 3, gate/up 3.7, down 3.  16 tokens, 52 us (103 MB, 16 us at
+// copy speed), and 32, 94 us: the instructions around the MMAs.  Eight codes take six to eight half-rate integer operations
 // and two MMAs of which one to three of eight columns are used; the integer pipe is busy 41 % of the time, issue 44 %, shared
 // memory and L1 33 %, DRAM a third.  No single one of them gives way: bringing the weights to L2 ahead of time, the
 // columns to L1 or registers, leaving the unused columns' loads out, or dropping the decoding altogether moves the down

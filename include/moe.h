@@ -400,6 +400,9 @@ size_t moe_stack_workspace_size(const moe_layer* layers, const moe_prerouter* he
  *   and at least moe_i8_row_bytes(in_dim), bases 16-byte aligned.  The bytes
  *   of a codes row from in_dim to moe_i8_row_bytes(in_dim) must be zero; those
  *   of a q row may hold anything (they are read and have no effect).
+ * Order: the product may be scheduled while the kernel before it in the stream
+ *   still runs, but reads nothing until that kernel is done: codes, scales and
+ *   biases may come from any work before the call, moe_quant_i8 included.
  */
 #define MOE_I8_MAX_IN 65536
 #define MOE_I8_MAX_OUT 1048576

@@ -40,10 +40,13 @@ struct QuantArgs {
   float* scale;
 };
 
-// A kernel that runs after the quantiser in a stream may start while it runs (programmatic launch): it reads the weights
-// early, and the codes, the scales and its output only after dependency_wait().
+// A kernel that runs after the quantiser in a stream may start while it runs (programmatic launch): it sets itself up and
+// asks for its first weights in L2, and reads or writes memory only after dependency_wait().  That holds for the weights
+// too: the quantiser's output is what a matrix is made of, so the kernel before may be writing them.  (A prefetch to L2
+// returns nothing, and L2 is where that kernel's writes arrive.)
 MOE_DEV void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 MOE_DEV void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+MOE_DEV void prefetch_to_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Eight neighbouring values of a row, or (VEC false: rows that are not aligned or not whole blocks) one.
 template <bool BF16, bool VEC>
@@ -197,7 +200,9 @@ constexpr int kRowWarps = 8;
 // Few tokens: a warp takes R weight rows, a lane every 32nd 16-byte chunk of them (of its part of K: KW warps split it
 // and add up in shared memory, so that enough loads are in flight when there are few rows), four dp4a a chunk, row and
 // token.  Bound by the weights' bytes; the tensor cores would add nothing to them (mma.sync s8, tried first, has its own
-// limit here: 27.7 us against 21.9 for one token x 2,048 -> 65,536, which is 6.1 TB/s).
+// limit here: 27.7 us against 19.0 for one token x 2,048 -> 65,536, which is 7.1 TB/s).  Eight loads of a lane go together,
+// where 16 leave room for half as many warps (22.3 us; behind the quantiser, 2,048 -> 4,096 6.1 against 4.7).  Without the
+// prefetch to L2 ahead of the wait the two take 21.8 and 5.3 us.
 template <int R, int NT>
 __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, int KW) {
   __shared__ int part[kRowWarps][R * NT];
@@ -211,8 +216,15 @@ __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, i
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[i][t] = 0;
-  constexpr int kAhead = 16 / R;  // chunks whose weights are loaded together
-  bool waited = false;
+  constexpr int kAhead = 8 / R;  // chunks whose weights are loaded together
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)  // the first of them into L2, a lane per 128 bytes
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (j * KW + kw) * 32 + lane;
+      if ((lane & 7) == 0 && c < a.K16) prefetch_to_l2(w[i] + 16 * static_cast<size_t>(c));
+    }
+  dependency_wait();
 #pragma unroll 1
   for (int c0 = kw * 32 + lane; c0 - lane < a.K16; c0 += 32 * KW * kAhead) {
     uint4 q[kAhead][R];
@@ -223,10 +235,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, i
         const int c = c0 + j * 32 * KW;
         q[j][i] = c < a.K16 ? ldg_stream(w[i] + 16 * static_cast<size_t>(c)) : make_uint4(0, 0, 0, 0);
       }
-    if (!waited) {
-      dependency_wait();
-      waited = true;
-    }
+    // one token: all of these loads before the codes' (mixed, 20.9 us for 2,048 -> 65,536 in place of 19.2); with more the
+    // codes' are as many, and best among them (two tokens, 2,048 -> 4,096: 5.0 us against 6.2)
+    if (NT == 1) __syncwarp();
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int c = min(c0 + j * 32 * KW, a.K16 - 1);
@@ -244,7 +255,6 @@ __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, i
       }
     }
   }
-  if (!waited) dependency_wait();
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -344,6 +354,11 @@ MOE_DEV void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint
       "[%4];" ::"r"(tc::sa(dst)),
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// The tile of a 2-D TMA load into L2 only.
+MOE_DEV void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
 
 MOE_DEV void cluster_sync() {
@@ -569,26 +584,20 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
   int fail = 0;
   auto parity = [](int i) { return static_cast<uint32_t>(i / kSplitStages) & 1u; };
   if (warp == 0 && lane == 0) {
-    // the first slices' weights do not wait for the codes
-    const int first = min(k1 - k0, kSplitStages);
+    // the first weights into L2 (32 tokens x 4,096 -> 4,096, weights out of cache: 10.4 us, 10.8 without)
 #pragma unroll 1
-    for (int n = 0; n < first; ++n) {
-      tc::bar_expect_tx(full + n, C::kStage);
-      tc::tma_load_2d(sm + n * C::kStage, &maps.w, (k0 + n) * kGK, m0, full + n);
-    }
+    for (int n = 0; n < min(k1 - k0, kSplitStages); ++n) tma_prefetch_2d(&maps.w, (k0 + n) * kGK, m0);
     dependency_wait();
     int n = 0;
 #pragma unroll 1
     for (; n < k1 - k0; ++n) {
       const int s = n % kSplitStages;
-      if (n >= kSplitStages) {
-        if (!tc::bar_wait(empty + s, parity(n) ^ 1u, a.timeout_ns)) {
-          fail = 1;
-          break;
-        }
-        tc::bar_expect_tx(full + s, C::kStage);
-        tc::tma_load_2d(sm + s * C::kStage, &maps.w, (k0 + n) * kGK, m0, full + s);
+      if (n >= kSplitStages && !tc::bar_wait(empty + s, parity(n) ^ 1u, a.timeout_ns)) {
+        fail = 1;
+        break;
       }
+      tc::bar_expect_tx(full + s, C::kStage);
+      tc::tma_load_2d(sm + s * C::kStage, &maps.w, (k0 + n) * kGK, m0, full + s);
       tc::tma_load_2d(sm + s * C::kStage + kGM * kGK, &maps.q, (k0 + n) * kGK, t0, full + s);
     }
 #pragma unroll 1

@@ -223,6 +223,42 @@ def test_quantised_projection_as_used(cuda_ok, T):
     assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("N,K,T", [
+    (4096, 2048, 1), (8192, 4096, 2), (1024, 1024, 4), (512, 512, 8),  # dp4a rows
+    (4096, 2048, 8), (2048, 2048, 64), (30000, 512, 16),  # K split over a cluster
+    (8192, 2048, 200), (4100, 4096, 600)])  # CTA pairs
+def test_matrix_that_the_quantiser_has_just_written(cuda_ok, N, K, T):
+    """The call right before the product writes the matrix's codes and scales, over those of another matrix: none of the
+    old ones may reach the product, eagerly or from a graph."""
+    g = torch.Generator(device=DEV).manual_seed(N + K + T)
+    x = torch.randn((T, K), device=DEV, generator=g)
+    q, sx = torch.empty((T, K), dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+    codes, sw = torch.zeros((N, K), dtype=torch.int8, device=DEV), torch.zeros(N, device=DEV)
+    lin = M.DeviceLinear8(codes, sw)
+    assert lin.codes.data_ptr() == codes.data_ptr()
+    Wf, out = torch.empty((N, K), device=DEV), torch.empty((T, N), device=DEV)
+
+    def call():
+        M.moe_quant_i8(x, q, sx)
+        M.moe_quant_i8(Wf, codes, sw)
+        M.moe_linear_i8(lin, q, sx, out, M.OUT_F32)
+
+    Wf.normal_(generator=g)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in range(12):
+        Wf.normal_(generator=g)
+        call() if i % 2 else graph.replay()
+        torch.cuda.synchronize()
+        first = out.clone()
+        assert torch.equal(codes.double(), codes_of(Wf)[0])
+        p, ref = product64(codes, sw, None, q, sx, K)
+        assert ((first.double() - ref).abs() <= 3.01 * EPS32 * p.abs()).all()
+
+
 def test_call_that_waits_for_room_in_the_queue(cuda_ok):
     """More calls than the device's queue holds, from two threads on their own streams: each waits without the
     interpreter's lock, and both results hold."""

@@ -1340,7 +1340,10 @@ struct StackWs {
   size_t bytes;
 };
 
-StackWs carve_stack(void* base, const moe_layer* L0, const moe_prerouter* P0, int T, int K, int K_next, size_t ll_bytes) {
+// (The layers share H, E, I and r, but each has adapters of its own, which decide its path and workspace.)
+StackWs carve_stack(void* base, const moe_layer* layers, int n_layers, const moe_prerouter* P0, int T, int K, int K_next,
+                    size_t ll_bytes) {
+  const moe_layer* L0 = &layers[0];
   StackWs w{};
   size_t off = 0;
   auto take = [&](size_t n) {
@@ -1358,9 +1361,10 @@ StackWs carve_stack(void* base, const moe_layer* L0, const moe_prerouter* P0, in
   w.pred1 = reinterpret_cast<int32_t*>(take(static_cast<size_t>(T) * K_next * 4));
   w.err = reinterpret_cast<int32_t*>(take(4));
   w.ll = reinterpret_cast<unsigned long long*>(take(ll_bytes));
-  w.ews_bytes = ws_bytes_for(L0, T, K);
-  if (T <= MOE_LAYER_DECODE_MAX_TOKENS) {  // path 4
-    const size_t one = carve_layer(nullptr, L0, T, K).bytes;
+  for (int l = 0; l < n_layers; ++l) {
+    const size_t e = ws_bytes_for(&layers[l], T, K);
+    const size_t one = T <= MOE_LAYER_DECODE_MAX_TOKENS ? carve_layer(nullptr, &layers[l], T, K).bytes : 0;  // path 4
+    if (e > w.ews_bytes) w.ews_bytes = e;
     if (one > w.ews_bytes) w.ews_bytes = one;
   }
   w.ews = take(w.ews_bytes);
@@ -1391,7 +1395,7 @@ int32_t moe_stack_grid(void) {
 size_t moe_stack_workspace_size(const moe_layer* layers, const moe_prerouter* heads, int32_t n_layers, int32_t T,
                                 int32_t K, int32_t K_next) {
   if (!layers || n_layers < 1 || T < 0 || T > MOE_MAX_TOKENS || K < 1) return 0;
-  return carve_stack(nullptr, &layers[0], heads, T, K, K_next, ll_bound(&layers[0], heads, K, n_layers)).bytes;
+  return carve_stack(nullptr, layers, n_layers, heads, T, K, K_next, ll_bound(&layers[0], heads, K, n_layers)).bytes;
 }
 
 moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads, int32_t n_layers, int32_t T,
@@ -1425,10 +1429,10 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
     if (s != MOE_OK) return s;
   }
   const size_t llb = ll_bound(&layers[0], heads, K, n_layers);
-  const StackWs need = carve_stack(nullptr, &layers[0], heads, T, K, K_next, llb);
+  const StackWs need = carve_stack(nullptr, layers, n_layers, heads, T, K, K_next, llb);
   if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < need.bytes) return MOE_ERR_WORKSPACE;
-  const StackWs ws = carve_stack(workspace, &layers[0], heads, T, K, K_next, llb);
+  const StackWs ws = carve_stack(workspace, layers, n_layers, heads, T, K, K_next, llb);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int H = layers[0].H, E = layers[0].E;
   int32_t* err = err_word ? err_word : ws.err;

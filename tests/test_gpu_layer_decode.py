@@ -485,6 +485,33 @@ def test_stack_path(cuda_ok, T, predicted):
         assert rel(after.double() - before.double(), out) <= tol
 
 
+@pytest.mark.parametrize("path", [M.PATH_LAYERS, M.PATH_LAYER_DECODE])
+@pytest.mark.parametrize("T", [1, 9])
+def test_stack_with_adapters_on_later_layers_only(cuda_ok, T, path):
+    """Layers share the shapes and not the adapters: one without routed adapters, one with them on the down projections,
+    one on gate and up too; a workspace of exactly the size that the query names."""
+    H, E, I, K = 512, 24, 256, 4
+    layers = [Layer(H, E, I, 16, seed=0), Layer(H, E, I, 16, down=True, seed=1),
+              Layer(H, E, I, 16, down=True, gate_up=True, seed=2)]
+    st = M.StackStructs([l.dev for l in layers])
+    x = tokens(T, H)
+    traces, u = torch.zeros((3, T, H), device=DEV), torch.zeros((3, T, H), dtype=torch.bfloat16, device=DEV)
+    idx = torch.zeros((3, T, K), dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = M.workspace(M.moe_stack_workspace_size(st, T, K, K))
+    M.moe_stack_decode(st, x, K, K, EPS, ws, x_trace=traces, u_trace=u, idx_all=idx, err_word=err,
+                       opts=M.stack_opts(path=path))
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    for l, L in enumerate(layers):
+        before, after = traces[l], traces[l + 1] if l + 1 < 3 else x
+        out = definition(L, u[l], K, idx[l])[3]
+        # the per-layer path multiplies fp16 operands, rounded weights and hidden values among them (2^-11 each)
+        tol = OUT_TOL + 1e-5 if path == M.PATH_LAYER_DECODE else 2e-3
+        tol += EPS32 * (after.double().norm(dim=1) / out.norm(dim=1)).max().item()
+        assert rel(after.double() - before.double(), out) <= tol
+
+
 def test_stack_path_refuses_many_tokens(cuda_ok):
     L = Layer(256, 16, 128, 8)
     st = M.StackStructs([L.dev])

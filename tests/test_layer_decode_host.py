@@ -73,6 +73,17 @@ def test_workspace_size(lib):
     assert size(4, ex_lora_A=A, ex_lora_B=A) > size(4)
 
 
+@pytest.mark.parametrize("T", [1, 4, 9, 32])
+@pytest.mark.parametrize("kw", [dict(ex_lora_A=A, ex_lora_B=A), dict(ex_lora_A_gu=A, ex_lora_B_gu=A)])
+def test_stack_workspace_holds_every_layers(lib, T, kw):
+    """A stack whose later layers alone have routed adapters needs as much as one where all of them do."""
+    def size(*layers):
+        return lib.moe_stack_workspace_size((_lib.moe_layer * len(layers))(*layers), None, len(layers), T, 4, 4)
+
+    assert size(layer(), layer(**kw), layer()) == size(layer(**kw), layer(**kw), layer(**kw))
+    assert size(layer(), layer(**kw)) >= lib.moe_layer_decode_workspace_size(ctypes.byref(layer(**kw)), T, 4)
+
+
 def test_binding_order_and_checks(rec):  # noqa: F811
     u, idx, w, out, work = u16(), i32(T, K), f32(T, K), f32(T, H), ws()
     M.moe_layer_decode(FakeLayer(), u, K, idx, w, out, M.OUT_F32, work, stream=0)

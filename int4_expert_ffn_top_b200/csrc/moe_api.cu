@@ -1433,6 +1433,14 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
   if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < need.bytes) return MOE_ERR_WORKSPACE;
   const StackWs ws = carve_stack(workspace, layers, n_layers, heads, T, K, K_next, llb);
+  if (opts && opts->path == 4) {  // what moe_layer_decode would refuse
+    if (!(eps >= 0.f) || !aligned(x, 16) || (u_trace && !aligned(u_trace, 16))) return MOE_ERR_INVALID_ARG;
+    // layer l executes pred_all's row l - 1 while it writes true_idx_all's row l
+    const size_t row = static_cast<size_t>(T) * K;
+    if (use_predicted_routing && n_layers > 1 && pred_all && true_idx_all && true_idx_all < pred_all &&
+        pred_all < true_idx_all + 2 * row)
+      return MOE_ERR_INVALID_ARG;
+  }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int H = layers[0].H, E = layers[0].E;
   int32_t* err = err_word ? err_word : ws.err;

@@ -84,6 +84,27 @@ def test_stack_workspace_holds_every_layers(lib, T, kw):
     assert size(layer(), layer(**kw)) >= lib.moe_layer_decode_workspace_size(ctypes.byref(layer(**kw)), T, 4)
 
 
+def test_stack_refuses_before_its_first_layer(lib):
+    """What moe_layer_decode refuses of a stack's buffers, path 4 refuses before anything is enqueued (here there is no
+    device to enqueue on: MOE_ERR_CUDA)."""
+    layers = (_lib.moe_layer * 3)(*[layer() for _ in range(3)])
+    head = _lib.moe_prerouter(A, A, A, A, 2048, 256, 64, 256)
+    heads = (_lib.moe_prerouter * 3)(head, head, head)
+    T, K, row = 2, 4, 2 * 4 * 4
+
+    def call(x=A, u=None, eps=1e-6, true=None, pred=None, path=4):
+        o = _lib.moe_stack_opts(0, path, 0, 0, None)
+        return lib.moe_stack_decode(layers, heads, 3, T, K, K, eps, x, None, u, None, true, pred, 1, A, ctypes.byref(o),
+                                    A, 1 << 30, None)
+
+    for kw in (dict(x=A + 4), dict(x=A + 8), dict(u=A + 8), dict(eps=-1.0), dict(eps=float("nan")),
+               dict(true=A, pred=A + row), dict(true=A, pred=A + row + 4), dict(true=A, pred=A + 4)):
+        assert call(**kw) == _lib.MOE_ERR_INVALID_ARG, kw
+    if not torch.cuda.is_available():
+        for kw in (dict(), dict(u=A), dict(true=A, pred=A), dict(true=A, pred=A + 2 * row), dict(true=A + 3 * row, pred=A)):
+            assert call(**kw) == _lib.MOE_ERR_CUDA, kw
+
+
 def test_binding_order_and_checks(rec):  # noqa: F811
     u, idx, w, out, work = u16(), i32(T, K), f32(T, K), f32(T, H), ws()
     M.moe_layer_decode(FakeLayer(), u, K, idx, w, out, M.OUT_F32, work, stream=0)

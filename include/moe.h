@@ -233,7 +233,9 @@ size_t moe_workspace_size(const moe_layer* L, int32_t T, int32_t K);
  *   22 significant bits; a finite hidden value beyond fp16's range (|h| > 65504)
  *   stores MOE_ERR_RANGE in err_word and leaves that token's output undefined.
  * workspace: at least moe_layer_decode_workspace_size(L, T, K) bytes, 256-byte
- *   aligned, contents on entry do not matter; calls that may overlap on the GPU
+ *   aligned, contents on entry do not matter (the barrier counters that a call
+ *   leaves for the next carry a tag each; where one does not hold, or a wait of
+ *   that call ran out, they are set up again); calls that may overlap on the GPU
  *   need workspaces of their own.  The launch needs every multiprocessor; two
  *   calls on different streams run one after the other or wait for each other's
  *   CTAs to leave, never in part.  Bounded waits as moe_expert_forward.
@@ -323,8 +325,8 @@ moe_status moe_tier_get_stats(const moe_tier* tier, moe_tier_stats* out);
 
 /* Options of moe_stack_decode (NULL = all defaults). */
 typedef struct {
-  int64_t timeout_ns;  /* bound on every device-side wait (single-launch kernel; per-layer grouped GEMMs);
-                          <= 0: 1 s for the single launch, 2 s for the GEMMs */
+  int64_t timeout_ns;  /* bound on every device-side wait (single-launch kernel; per-layer grouped GEMMs; path 4);
+                          <= 0: 1 s for the single launch, 2 s for the others */
   int32_t path;        /* 0: automatic; 1: per-layer launches; 2: single-launch kernel (MOE_ERR_UNSUPPORTED if
                           the shapes are not eligible); 3: the first-generation single-launch kernel (kept for
                           comparison); 4: per layer, norm to combine in one moe_layer_decode launch
@@ -333,8 +335,9 @@ typedef struct {
   int32_t test_drop_cta;    /*   test_drop_cta never publishes its residual rows of layer L-1, so the other CTAs'
                                  bounded waits run out; on the per-layer path the CTA test_drop_cta of layer L-1's
                                  gate/up grouped GEMM (tensor-core path only) never marks its first operand stage
-                                 full, so the MMA's bounded wait runs out.  Either way err_word reports
-                                 MOE_ERR_TIMEOUT */
+                                 full, so the MMA's bounded wait runs out; on path 4 the CTA test_drop_cta of
+                                 layer L-1's launch starts four limits late, so the others' waits run out.  Either
+                                 way err_word reports MOE_ERR_TIMEOUT */
   int64_t* trace;           /* optional device buffer [n_layers][moe_stack_grid()][16] of int64 %globaltimer
                                stamps (ns) per CTA of the single-launch kernel (paths 0 and 2), written by its
                                thread 0: 0 x received, 1 RMSNorm done and layer weights landed, 2 router /

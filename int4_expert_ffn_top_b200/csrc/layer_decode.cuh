@@ -104,6 +104,7 @@ struct Args {
   float* tex;         // [T K][r]
   int* err;
   long long timeout_ns;
+  int late_cta;       // test hook: this CTA starts four limits late (-1: none)
   int smem_image;     // every CTA forms the tokens' images in shared memory; else CTA t forms token t's, in img
   Smem sm;
 };
@@ -144,37 +145,59 @@ MOE_DEV float lo_half(uint32_t v) { return half_bits_to_float(static_cast<uint16
 MOE_DEV float hi_half(uint32_t v) { return half_bits_to_float(static_cast<uint16_t>(v >> 16)); }
 
 // ----------------------------------------------------------------------------- grid barrier
-// The header of the workspace: counters (one per barrier, one of CTAs that are through), between two marks that say
-// that the counters were left at zero.  The last CTA of a call leaves them so; where the marks do not hold (a new
-// workspace, or one that something else has written over) CTA 0 sets the header up before any CTA counts.
+// The header of the workspace: a word per barrier, one for the CTAs that are through with every barrier, and a mark.  A
+// word is a tag (48 bits, of its place and the workspace's address) over a count (16 bits).  The last CTA of a call
+// leaves every count at zero, so a header whose tags all hold is ready; where one does not (a new workspace, or one that
+// something else has written to) CTA 0 sets the header up: it zeroes the words whose tags hold, then writes the others, so
+// that a CTA that finds every tag good, in whatever order it reads them, counts on zeros.
+// A CTA that gave up waiting for the tags leaves without counting.  One whose wait at a barrier ran out goes on, makes its
+// counts and takes the mark away.  If CTA 0 sets the header up after that (it was late), it wipes out counts at a barrier
+// (the mark and the CTAs that are through it writes before the barriers, and a CTA counts there last), its own wait there
+// runs out, and the mark goes after everything else.  The next call finds no mark and sets the header up again.
 struct Header {
-  unsigned long long mark0;
-  uint32_t count[kBars + 1];  // [kBars]: CTAs that are through with every barrier
-  unsigned long long mark1;
+  unsigned long long word[kBars + 2];  // [kBars]: CTAs that are through, [kBars + 1]: the mark
 };
 static_assert(sizeof(Header) <= kHeaderBytes, "header");
 
-__device__ __noinline__ void header_ready(Header* h, volatile int* failed, int* err, long long timeout_ns) {
-  const unsigned long long m0 = 0x6c617965725f6465ull ^ reinterpret_cast<unsigned long long>(h), m1 = ~m0;
-  volatile Header* v = h;
-  if (v->mark0 == m0 && v->mark1 == m1) return;
-  if (blockIdx.x == 0) {
-    for (int i = 0; i <= kBars; ++i) v->count[i] = 0;
-    __threadfence();
-    v->mark1 = m1;
-    v->mark0 = m0;
-    __threadfence();
-    return;
-  }
-  const long long end = gtime() + timeout_ns;
-  while (v->mark0 != m0 || v->mark1 != m1) {
-    if (gtime() > end) {
-      *failed = 1;
-      report(err, 5 /* MOE_ERR_TIMEOUT */);
-      break;
+MOE_DEV unsigned long long header_word(const Header* h, int i, unsigned count) {
+  return ((0x6c617965725full ^ (reinterpret_cast<unsigned long long>(h) >> 8)) + static_cast<unsigned>(i)) << 16 | count;
+}
+
+MOE_DEV uint32_t header_holds(const Header* h) {  // a bit per word
+  const volatile Header* v = h;
+  unsigned long long w[kBars + 2];
+#pragma unroll
+  for (int i = 0; i < kBars + 2; ++i) w[i] = v->word[i];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kBars + 2; ++i) m |= static_cast<uint32_t>(w[i] >> 16 == header_word(h, i, 0) >> 16) << i;
+  return m;
+}
+
+// False: this CTA gave up.
+__device__ __noinline__ bool header_ready(Header* h, int* err, long long timeout_ns) {
+  constexpr uint32_t kAll = (1u << (kBars + 2)) - 1;
+  const uint32_t m = header_holds(h);
+  if (m != kAll) {
+    if (blockIdx.x == 0) {
+      volatile Header* v = h;
+      for (int pass = 0; pass < 2; ++pass)
+        for (int i = kBars + 1; i >= 0; --i)
+          if (((m >> i) & 1) == static_cast<uint32_t>(1 - pass)) {
+            v->word[i] = header_word(h, i, 0);
+            __threadfence();
+          }
+    } else {
+      const long long end = gtime() + timeout_ns;
+      while (header_holds(h) != kAll) {
+        if (gtime() > end) {
+          report(err, 5 /* MOE_ERR_TIMEOUT */);
+          return false;
+        }
+      }
     }
   }
-  __threadfence();
+  return true;  // (the release with which the CTA counts keeps its counts behind these reads, so behind CTA 0's zeros)
 }
 
 // Each CTA adds one to a barrier's counter when its part is written and goes on when the counter has reached the
@@ -186,29 +209,37 @@ __device__ __noinline__ void header_ready(Header* h, volatile int* failed, int* 
 MOE_DEV void grid_arrive(Header* h, int b) {
   named_sync(15, kThreads);
   if (threadIdx.x == 0)
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(h->count + b) : "memory");
+    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(h->word + b) : "memory");
 }
 
 __device__ __noinline__ void grid_wait(Header* h, int b, bool last, volatile int* failed, int* err,
                                        long long timeout_ns) {
   if (threadIdx.x == 0) {
-    const uint32_t* c = h->count + b;
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
-    if (v < gridDim.x) {
+    const unsigned long long *c = h->word + b, full = header_word(h, b, gridDim.x);
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(c) : "memory");
+    if (v < full) {
       const long long end = gtime() + timeout_ns;
       for (;;) {
-        asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
-        if (v >= gridDim.x || *failed) break;
+        asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(c) : "memory");
+        if (v >= full || *failed) break;
         if (gtime() > end) {
           *failed = 1;
           report(err, 5 /* MOE_ERR_TIMEOUT */);
         }
       }
     }
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
-    if (last && atomicAdd(h->count + kBars, 1u) == gridDim.x - 1) {  // no CTA reads the counters any more
-      for (int i = 0; i <= kBars; ++i) *reinterpret_cast<volatile uint32_t*>(h->count + i) = 0;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(c) : "memory");
+    if (last) {
+      volatile Header* w = h;
+      if (*failed) __threadfence();
+      if (atomicAdd(h->word + kBars, 1ull) == header_word(h, kBars, gridDim.x - 1)) {  // no CTA reads the counts any more
+        for (int i = 0; i <= kBars; ++i) w->word[i] = header_word(h, i, 0);
+      }
+      if (*failed) {
+        __threadfence();
+        w->word[kBars + 1] = 0;
+      }
     }
   }
   named_sync(15, kThreads);
@@ -696,8 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
   const int nblk = (T + 7) / 8;
 
   if (tid == kThreads - 32) {
-    misc[0] = 0;
-    header_ready(a.bar, misc, a.err, a.timeout_ns);
+    if (cta == a.late_cta)
+      for (const long long end = gtime() + 4 * a.timeout_ns; gtime() < end;) __nanosleep(1000);
+    misc[0] = header_ready(a.bar, a.err, a.timeout_ns) ? 0 : 1;
   }
   // --------------------------------------------------------------------------- weights that no token decides
   // The first shared tile's units: unit warp % U for token blocks warp / U, + sh_n, ...
@@ -748,22 +780,30 @@ __global__ void __launch_bounds__(kThreads, 1) layer_decode_kernel(const __grid_
     else
       build_image<false>(a, t, wi, warps, team, red, row, u, c, write_u);
   };
+  auto gave_up = [&]() {  // on the header (the whole CTA)
+    named_sync(15, kThreads);
+    if (!*failed) return false;
+    cp_wait<0>();
+    return true;
+  };
   if (!a.smem_image) {
     if (cta < T)
       build(cta, warp, kWarps, 0, a.img + static_cast<size_t>(cta) * ldu, a.us + cta * G, a.ic + cta, true);
+    if (gave_up()) return;
     grid_arrive(a.bar, B_IMAGE);
     grid_wait(a.bar, B_IMAGE, false, failed, a.err, a.timeout_ns);
 #pragma unroll 1
     for (int i = tid; i < T * G; i += kThreads) us[i] = __ldcg(a.us + i);
     if (tid < T) ic[tid] = __ldcg(a.ic + tid);
+    named_sync(15, kThreads);
   } else {
     int logW = 0;  // at most 4 tokens
     while (T << (logW + 1) <= kWarps) ++logW;
     const int W = 1 << logW, team = warp >> logW;
     if (team < T)
       build(team, warp & (W - 1), W, team, sm + S.img + team * ldu, us + team * G, ic + team, team == cta);
+    if (gave_up()) return;
   }
-  named_sync(15, kThreads);
 
   // --------------------------------------------------------------------------- rows over all tokens: router, shared
   // gate (8 bits), the shared expert's gate and up LoRA A (fp16)

@@ -890,11 +890,11 @@ int layer_grid() {
   return n;
 }
 
-// moe_layer_decode with the bound of its waits exposed (the stack passes its option through).
+// moe_layer_decode with the bound of its waits and the test hook exposed (the stack passes its options through).
 moe_status layer_decode_entry(const moe_layer* L, uint16_t* u, const float* x, float eps, int32_t T, int32_t K,
                               const int32_t* exec_idx, float* logits, int32_t* idx, float* w, void* out,
                               int32_t out_mode, void* workspace, size_t ws_bytes, int32_t* err_word,
-                              long long timeout_ns, void* stream) {
+                              long long timeout_ns, int late_cta, void* stream) {
   moe_status s = check_layer(L, T, K);
   if (s != MOE_OK) return s;
   if (T > MOE_LAYER_DECODE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
@@ -960,6 +960,7 @@ moe_status layer_decode_entry(const moe_layer* L, uint16_t* u, const float* x, f
   a.tex = ws.tex;
   a.err = err_word;
   a.timeout_ns = timeout_ns;
+  a.late_cta = late_cta;
   // Images in every CTA's shared memory save a barrier and cost every CTA the whole norm: 3 and 4 tokens of the 35B shape
   // 26.8 and 30.5 us against 28.4 and 32.4; 8 tokens 40.9 either way, and the 8B shape's rows are longer.
   a.smem_image = T <= 4;
@@ -984,7 +985,7 @@ moe_status moe_layer_decode(const moe_layer* L, uint16_t* u, const float* x, flo
                             const int32_t* exec_idx, float* logits, int32_t* idx, float* w, void* out, int32_t out_mode,
                             void* workspace, size_t ws_bytes, int32_t* err_word, void* stream) {
   return layer_decode_entry(L, u, x, eps, T, K, exec_idx, logits, idx, w, out, out_mode, workspace, ws_bytes, err_word,
-                            kGemmTimeoutNs, stream);
+                            kGemmTimeoutNs, -1, stream);
 }
 
 }  // extern "C"
@@ -1483,11 +1484,12 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
     int32_t* idx_true = true_idx_all ? true_idx_all + l * TK : (idx_all && !use_predicted_routing ? idx_all + l * TK
                                                                                                     : ws.idx_true);
     const int32_t* idx_exec = use_predicted_routing && l > 0 ? pred_prev : idx_true;
+    const long long limit = (opts && opts->timeout_ns > 0) ? opts->timeout_ns : kGemmTimeoutNs;
+    const int drop = (opts && opts->test_drop_layer == l + 1) ? opts->test_drop_cta : -1;
     moe_status s;
     if (want == 4) {
       s = layer_decode_entry(L, u, x, eps, T, K, idx_exec == idx_true ? nullptr : idx_exec, ws.logits, idx_true, ws.w, x, 2,
-                             ws.ews, ws.ews_bytes, err,
-                             (opts && opts->timeout_ns > 0) ? opts->timeout_ns : kGemmTimeoutNs, stream);
+                             ws.ews, ws.ews_bytes, err, limit, drop, stream);
       if (s != MOE_OK) return s;
     } else {
       s = moe_rmsnorm_bf16(x, T, H, eps, u, stream);
@@ -1501,10 +1503,7 @@ moe_status moe_stack_decode(const moe_layer* layers, const moe_prerouter* heads,
         cudaMemcpyAsync(idx_all + l * TK, idx_exec, TK * 4, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
       return MOE_ERR_CUDA;
     if (want != 4) {
-      const long long gemm_to = (opts && opts->timeout_ns > 0) ? opts->timeout_ns : kGemmTimeoutNs;
-      const int drop = (opts && opts->test_drop_layer == l + 1) ? opts->test_drop_cta : -1;
-      s = expert_forward_entry(L, u, T, K, idx_exec, ws.w, x, 2, nullptr, ws.ews, ws.ews_bytes, err, gemm_to, drop,
-                               stream);
+      s = expert_forward_entry(L, u, T, K, idx_exec, ws.w, x, 2, nullptr, ws.ews, ws.ews_bytes, err, limit, drop, stream);
       if (s != MOE_OK) return s;
     }
     if (heads) {

@@ -356,6 +356,58 @@ def test_repeats_streams_and_graphs(cuda_ok):
         assert c.err.item() == 0
 
 
+@pytest.mark.parametrize("T", [2, 9])
+def test_workspace_written_to_in_part(cuda_ok, T):
+    """Any four bytes of what a call leaves at the head of its workspace written over: the next call is as the first."""
+    L = Layer(512, 24, 256, 16, down=True)
+    x = tokens(T, 512)
+    c = Call(L, T, 4)(x=x)
+    torch.cuda.synchronize()
+    first = c.out.clone()
+    words = c.ws[:64].view(torch.int32)
+    for i in range(16):
+        for v in (0, 1, 148, -1, 0x10000):
+            words[i] = v
+            c.out.zero_()
+            c(x=x)
+            torch.cuda.synchronize()
+            assert torch.equal(c.out, first) and c.err.item() == 0, (i, v)
+    words.zero_()
+    c(x=x)
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, first) and c.err.item() == 0
+
+
+@pytest.mark.parametrize("late", [0, 1, 147])
+@pytest.mark.parametrize("fresh", [False, True])
+@pytest.mark.parametrize("T,routed", [(2, False), (2, True), (9, True)])
+def test_waits_that_run_out(cuda_ok, T, routed, fresh, late):
+    """One CTA four limits late: the others' waits (at a barrier, or for CTA 0 to set a fresh workspace's counters up) run
+    out and say so, the call ends, and the next ones on the same workspace are as if it had not been."""
+    H, K = 512, 4
+    layers = [Layer(H, 24, 256, 16, down=routed, gate_up=routed, seed=s) for s in range(2)]
+    st = M.StackStructs([l.dev for l in layers])
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = M.workspace(M.moe_stack_workspace_size(st, T, K, K))
+    x0 = tokens(T, H)
+
+    def run(**kw):
+        x = x0.clone()
+        M.moe_stack_decode(st, x, K, K, EPS, ws, err_word=err, opts=M.stack_opts(path=M.PATH_LAYER_DECODE, **kw))
+        torch.cuda.synchronize()
+        return x, err.item()
+
+    good, code = run()
+    assert code == 0
+    for layer in (0, 1, 0):
+        if fresh:
+            ws.fill_(0xA5)
+        assert run(timeout_ns=2_000_000, drop_layer=layer, drop_cta=late)[1] == _lib.MOE_ERR_TIMEOUT
+        for _ in range(3):
+            x, code = run()
+            assert code == 0 and torch.equal(x, good)
+
+
 def test_two_calls_at_once(cuda_ok):
     """Two streams, each with its own workspace, many calls in flight."""
     L = Layer(512, 24, 256, 16)

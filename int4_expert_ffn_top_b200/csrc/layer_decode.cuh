@@ -27,9 +27,13 @@
 // 3 % faster (35B shape, 1 / 16 / 32 tokens in a graph: 21.9 / 51.3 / 93 us, 22.2 / 51.8 / 94).
 //
 // Precision.  u (bf16, 8 significant bits) is exact in fp16 after scaling each token
-// by a power of two that puts its largest entry in [2^9, 2^10); hidden values h are
-// stored as two fp16 numbers, hi and 2^11 (h - hi), 22 bits together, in two columns
-// of the N side.  Products are exact, group sums and everything after are fp32.
+// by a power of two that puts its largest entry in [2^9, 2^10) (entries under 2^-22 of
+// it lose bits: 2^-30 of it at most); hidden values h are stored as two fp16 numbers, hi
+// and 2^11 (h - hi), 22 bits together, in two columns of the N side.  They are stored
+// unscaled: below 2^-14 what stays is an absolute 2^-36.  A power of two for each row
+// would need the row's largest value, which only another exchange between all CTAs gives
+// (1.1 us and more of 22), and behind a norm no hidden vector is that small.
+// Products are exact, group sums and everything after are fp32.
 //
 // What bounds it (B200, 35B shape).  One token, 22 us: the chain of steps; 9.7 MB of weights take 1.5 us, five
 // barriers and hand-overs 1.1 us and more each, the top-K 3, gate/up 3.7, down 3.  16 tokens, 52 us (103 MB, 16 us at

@@ -284,6 +284,34 @@ def test_magnitudes_of_u(cuda_ok, mag):
     assert (c.out[2] == 0).all()
 
 
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("mag,share", [(1e-2, 1e-6), (1e-3, 1e-4), (1e-4, 1e-2)])
+def test_small_tokens_keep_what_the_header_says(cuda_ok, mag, share, down):
+    """Hidden values under 2^-14 are rounded by at most 2^-36 each: a vector of I of them by sqrt(I) 2^-36, which the down
+    projection (with its adapter) stretches by its largest singular value at most; the K experts' weights add up to 1, the
+    shared expert's gate is at most 1.  `share` of the output bounds all of it, so an output that is lost fails."""
+    H, I, K, T = 512, 128, 3, 5
+    L = Layer(H, 16, I, 8, down=down)
+    u = (tokens(T, H, spread=False) * mag).bfloat16()
+    c = Call(L, T, K)(u=u)
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    out = definition(L, u, K, c.idx)[3]
+    cut = 2 * I * M.qrow_bytes(H, 4)
+
+    def stretch(block, p):
+        D = matrix(block[cut:cut + H * M.qrow_bytes(I, 4)].view(H, -1), I, 4)
+        if p is not None:
+            D = D + p[1].double() @ p[0].double()
+        return torch.linalg.matrix_norm(D, 2).item()
+
+    most = max(stretch(L.pool[e], (L.down[0][e], L.down[1][e]) if down else None) for e in range(16))
+    floor = (most + stretch(L.shared, L.sh[2])) * I ** 0.5 * 2.0 ** -36
+    n = out.norm(dim=1)
+    assert (floor <= share * n).all()
+    assert ((c.out.double() - out).norm(dim=1) <= (OUT_TOL + 1e-5) * n + floor).all()
+
+
 def test_non_finite_tokens_stay_alone(cuda_ok):
     """NaN and infinite entries make their own token NaN; ids stay in range; the others are as without them."""
     L = Layer(512, 16, 128, 8, down=True, gate_up=True)

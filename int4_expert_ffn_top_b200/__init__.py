@@ -152,13 +152,18 @@ def moe_layer_decode(layer: DeviceLayer, u: torch.Tensor | None, K: int, idx: to
 
     Without ``x``, ``u`` (bf16 ``[T, H]``) is the input; with ``x`` (fp32 ``[T, H]``) it receives bf16(rmsnorm(x)),
     or is None.  ``exec_idx`` executes these experts instead of the router's own top-K, which ``idx`` receives.
+    The layer is on the current device, like every tensor.
     """
-    fn, L = "moe_layer_decode", layer.struct
-    if stream is None:
-        code = _lib.binding().layer(ctypes.addressof(L), u, x, eps, K, exec_idx, logits, idx, w, out, out_mode, workspace,
-                                    err_word)
+    fn, L, dev = "moe_layer_decode", layer.struct, getattr(layer, "device", None)
+    if stream is None and dev is not None:
+        code = _lib.binding().layer(ctypes.addressof(L), dev.index, u, x, eps, K, exec_idx, logits, idx, w, out, out_mode,
+                                    workspace, err_word)
         if code is not None:
             return _check(fn, code)
+    if isinstance(layer, TieredPool):
+        raise ValueError(f"{fn}: a TieredPool's slots are no experts that the router knows; use moe_expert_forward")
+    if dev is not None and dev.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the layer is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
     if x is None:
         T = _rows(fn, "u", u, L.H, BF16_BITS)
     else:

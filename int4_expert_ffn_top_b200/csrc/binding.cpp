@@ -140,31 +140,32 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
 }
 
-// layer(address of the moe_layer, u | None, x | None, eps, K, exec_idx | None, logits | None, idx, w, out, out_mode,
+// layer(address of the moe_layer, its device, u | None, x | None, eps, K, exec_idx | None, logits | None, idx, w, out, out_mode,
 // workspace, err_word | None) -> status | None
 PyObject* layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 13 || !p_layer) return none();
+  if (n != 14 || !p_layer) return none();
   try {
     const auto* L = static_cast<const moe_layer*>(PyLong_AsVoidPtr(a[0]));
-    const double eps = PyFloat_AsDouble(a[3]);
-    const long K = PyLong_AsLong(a[4]), mode = PyLong_AsLong(a[10]);
+    const double eps = PyFloat_AsDouble(a[4]);
+    const long layer_dev = PyLong_AsLong(a[1]), K = PyLong_AsLong(a[5]), mode = PyLong_AsLong(a[11]);
     if (PyErr_Occurred()) {
       PyErr_Clear();
       return none();
     }
     if (!L || K < 1 || K > 8 || mode < 0 || mode > 2) return none();
     const int dev = c10::cuda::current_device();
-    const bool norm = a[2] != Py_None;
-    const at::Tensor* rows = tensor(norm ? a[2] : a[1], norm ? F32 : BF16, 0, dev);
+    if (layer_dev != dev) return none();
+    const bool norm = a[3] != Py_None;
+    const at::Tensor* rows = tensor(norm ? a[3] : a[2], norm ? F32 : BF16, 0, dev);
     if (!rows || rows->dim() != 2 || rows->size(1) != L->H || rows->size(0) > MOE_LAYER_DECODE_MAX_TOKENS) return none();
     const int64_t T = rows->size(0);
     void *u, *exec, *logits, *idx, *w, *out, *ws, *err;
-    if (!address(a[1], BF16, T * L->H, dev, &u, norm) || !address(a[5], I32, T * K, dev, &exec, true) ||
-        !address(a[6], F32, T * L->E, dev, &logits, true) || !address(a[7], I32, T * K, dev, &idx) ||
-        !address(a[8], F32, T * K, dev, &w) || !address(a[9], mode == 1 ? BF16 : F32, T * L->H, dev, &out) ||
-        !address(a[11], BYTES, 0, dev, &ws) || !address(a[12], I32, 1, dev, &err, true))
+    if (!address(a[2], BF16, T * L->H, dev, &u, norm) || !address(a[6], I32, T * K, dev, &exec, true) ||
+        !address(a[7], F32, T * L->E, dev, &logits, true) || !address(a[8], I32, T * K, dev, &idx) ||
+        !address(a[9], F32, T * K, dev, &w) || !address(a[10], mode == 1 ? BF16 : F32, T * L->H, dev, &out) ||
+        !address(a[12], BYTES, 0, dev, &ws) || !address(a[13], I32, 1, dev, &err, true))
       return none();
-    const at::Tensor& wt = THPVariable_Unpack(a[11]);
+    const at::Tensor& wt = THPVariable_Unpack(a[12]);
     const cudaStream_t st = stream(dev);
     const size_t ws_bytes = static_cast<size_t>(wt.numel()) * wt.element_size();
     const float* px = norm ? static_cast<const float*>(rows->data_ptr()) : nullptr;

@@ -102,6 +102,7 @@ class DeviceLayer:
         if pool is None:
             pool = torch.zeros(E * self.stride, dtype=torch.uint8, device=device)
         self.pool = pool
+        self.device = pool.device
         self.fill_experts(host["experts"])
         ex_lora = [e for e in host["experts"].values() if "down_lora" in e]
         if cfg.lora_routed_down:
@@ -159,6 +160,7 @@ class DeviceLayer:
         self = cls.__new__(cls)
         self.cfg = SimpleNamespace(H=H, E=E, I=I, I_s=I, r=r)
         self.stride = pool.shape[1]
+        self.device = dev
         self.pool = take("pool", pool, torch.uint8, (E, self.stride), 256)
         rec8 = qrow_bytes(H, 8)
         t = self.t = {"router": take("router", router, torch.uint8, (E, rec8)),

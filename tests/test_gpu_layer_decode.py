@@ -258,6 +258,16 @@ def test_no_logits_and_no_tokens(cuda_ok):
     M.moe_layer_decode(L.dev, u[:0], 2, c.idx, c.w, c.out, 0, c.ws)
 
 
+def test_layer_said_to_be_elsewhere(cuda_ok):
+    L = Layer(256, 16, 128, 0)
+    c = Call(L, 3, 2)
+    L.dev.device = torch.device("cuda", torch.cuda.current_device() + 1)
+    with pytest.raises(ValueError, match="the layer is on"):
+        c(u=tokens(3, 256).bfloat16())
+    torch.cuda.synchronize()
+    assert (c.idx == -1).all() and (c.buf == 7).all()
+
+
 # ----------------------------------------------------------------------------- values
 @pytest.mark.parametrize("mag", [1e-36, 1e-8, 3.0, 1e3])
 def test_magnitudes_of_u(cuda_ok, mag):

@@ -128,6 +128,21 @@ def test_binding_order_and_checks(rec):  # noqa: F811
     assert len(rec.calls) == n
 
 
+def test_layer_of_another_device_is_refused(rec):  # noqa: F811
+    class There(FakeLayer):
+        device = torch.device("cuda", 1)
+
+    u, idx, w, out, work = u16(), i32(T, K), f32(T, K), f32(T, H), ws()
+    for stream in (None, 0):
+        with pytest.raises(ValueError, match="layer is on cuda:1"):
+            M.moe_layer_decode(There(), u, K, idx, w, out, M.OUT_F32, work, stream=stream)
+    slots = object.__new__(M.TieredPool)
+    slots.struct = FakeLayer().struct
+    with pytest.raises(ValueError, match="TieredPool"):
+        M.moe_layer_decode(slots, u, K, idx, w, out, M.OUT_F32, work, stream=0)
+    assert not rec.calls
+
+
 def test_layer_from_tensors():
     h, e, i, r = 256, 4, 128, 8
     t = dict(router=torch.zeros((e, M.qrow_bytes(h, 8)), dtype=torch.uint8),
@@ -149,6 +164,7 @@ def test_layer_from_tensors():
     assert (s.H, s.E, s.I, s.I_s, s.r, s.expert_stride, s.lora_scale) == (h, e, i, i, r, t["pool"].shape[1], 0.5)
     assert s.pool == t["pool"].data_ptr() and s.sh_lora_A[0] == sh[0][0].data_ptr() and s.sh_lora_A[1] is None
     assert s.router_bias is None and s.ex_lora_A and not s.ex_lora_A_gu
+    assert L.device == t["pool"].device
     for bad in (dict(router=t["router"][:-1]), dict(pool=t["pool"][:, :-16]), dict(shared_block=t["shared_block"][:512]),
                 dict(shared_lora=[(ab(r, h), ab(i, r + 1)), None, None]), dict(router_bias=torch.zeros(e + 1)),
                 dict(routed_down_lora=(ab(e, r, i).float(), ab(e, h, r)))):

@@ -12,7 +12,8 @@ namespace {
 
 using namespace moe;
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }  // (null: yes)
+inline bool aligned16(const void* p) { return aligned(p, 16); }
 
 moe_status launched() { return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -172,7 +173,8 @@ moe_status moe_quant_i8(const void* x, int32_t x_type, int32_t T, int32_t H, flo
   if (T < 0 || T > MOE_MAX_TOKENS || !dim_ok(H)) return MOE_ERR_UNSUPPORTED;
   if (ldq < row_bytes(H) || ldq % 16) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (!x || !q || !scale || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (!x || !q || !scale || !aligned16(q) || !aligned(x, x_type == 1 ? 2 : 4) || !aligned(scale, 4))
+    return MOE_ERR_INVALID_ARG;
   l8::QuantArgs a{x, T, H, eps, q, ldq, scale};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // whole 8-value pieces: rows that begin on 16 bytes (and their codes on 8)
@@ -191,9 +193,12 @@ moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, con
     return MOE_ERR_UNSUPPORTED;
   const int64_t need = row_bytes(W->in_dim);
   if (W->ld < need || W->ld % 16 || ldq < need || ldq % 16) return MOE_ERR_INVALID_ARG;
-  if (!W->codes || !W->scale || !aligned16(W->codes)) return MOE_ERR_INVALID_ARG;
+  if (!W->codes || !W->scale || !aligned16(W->codes) || !aligned(W->scale, 4) || !aligned(W->bias, 4))
+    return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (!q || !qscale || !out || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (!q || !qscale || !out || !aligned16(q) || !aligned(qscale, 4) || !aligned(out, out_mode == 1 ? 2 : 4) ||
+      !aligned(err_word, 4))
+    return MOE_ERR_INVALID_ARG;
   l8::LinArgs a{};
   a.W = W->codes;
   a.ldw = W->ld;

@@ -901,6 +901,11 @@ moe_status layer_decode_entry(const moe_layer* L, uint16_t* u, const float* x, f
   if (out_mode < 0 || out_mode > 2 || (x && !(eps >= 0.f))) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if ((!u && !x) || !idx || !w || !out || (u && !aligned(u, 16)) || (x && !aligned(x, 16))) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(idx), static_cast<const void*>(w), static_cast<const void*>(logits),
+                        static_cast<const void*>(exec_idx), static_cast<const void*>(err_word),
+                        static_cast<const void*>(L->router_bias), static_cast<const void*>(out_mode == 1 ? nullptr : out)})
+    if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(out, 2)) return MOE_ERR_INVALID_ARG;
   // every CTA reads exec_idx after one has written idx
   if (exec_idx && exec_idx < idx + T * K && idx < exec_idx + T * K) return MOE_ERR_INVALID_ARG;
   s = check_expert_weights(L);

@@ -53,6 +53,24 @@ def test_refusals(lib):
         assert call(lib, layer(**kw)) == uns, kw
 
 
+def test_addresses_that_no_element_can_have(lib):
+    """fp32 and int32 at multiples of 4 bytes, bf16 of 2: the kernels' accesses would fault on anything else."""
+    L = layer()
+    ok = dict(ex=None, logits=None, idx=A, w=A, out=A, mode=0, err=None)
+
+    def call(L=L, **kw):
+        a = ok | kw
+        return lib.moe_layer_decode(ctypes.byref(L), A, None, 0.0, 2, 4, a["ex"], a["logits"], a["idx"], a["w"], a["out"],
+                                    a["mode"], A, 16, a["err"], None)
+
+    far = A + 4096
+    for kw in (dict(ex=far + 2), dict(logits=far + 1), dict(idx=A + 2), dict(w=A + 1), dict(out=A + 2), dict(out=A + 2, mode=2),
+               dict(out=A + 1, mode=1), dict(err=far + 2), dict(L=layer(router_bias=A + 2))):
+        assert call(**kw) == _lib.MOE_ERR_INVALID_ARG, kw
+    for kw in (dict(ex=far + 4), dict(logits=far + 4), dict(out=A + 4), dict(out=A + 2, mode=1), dict(err=far + 4)):
+        assert call(**kw) == _lib.MOE_ERR_WORKSPACE, kw  # as far as the workspace check
+
+
 def test_given_experts_apart_from_the_routers(lib):
     """exec_idx is read by every CTA after idx is written by one: the two may not overlap."""
     L = layer()

@@ -64,6 +64,17 @@ def test_library_refuses_bad_calls(lib):
         assert product(**kw) == uns, kw
 
 
+def test_library_refuses_addresses_that_no_element_can_have(lib):
+    bad, A = _lib.MOE_ERR_INVALID_ARG, 1 << 20
+    for kind, x, scale in ((0, A + 2, A), (0, A + 1, A), (1, A + 1, A), (0, A, A + 2), (1, A + 2, A + 1)):
+        assert lib.moe_quant_i8(x, kind, 1, 64, -1.0, A, 64, scale, None) == bad
+    for scale, bias, qs, out, mode, err in ((A + 2, None, A, A, 0, None), (A, A + 1, A, A, 0, None), (A, None, A + 2, A, 0, None),
+                                            (A, None, A, A + 2, 0, None), (A, None, A, A + 2, 2, None),
+                                            (A, None, A, A + 1, 1, None), (A, None, A, A, 0, A + 2)):
+        W = _lib.moe_linear8(A, 64, scale, bias, 8, 64)
+        assert lib.moe_linear_i8(ctypes.byref(W), A, 64, qs, 1, out, mode, err, None) == bad
+
+
 class FakeLinear:
     def __init__(self, n, k):
         self.struct = _lib.moe_linear8(1 << 20, (k + 15) // 16 * 16, 1 << 20, None, n, k)

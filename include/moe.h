@@ -445,6 +445,7 @@ moe_status moe_quant_i8(const void* x, int32_t x_type, int32_t T, int32_t H, flo
 /*
  * The product above for T tokens: q [T] rows of ldq bytes, qscale [T], out
  * [T][out_dim].  out_mode 0: fp32; 1: bf16; 2: fp32, added to what out holds.
+ * Bounded waits as moe_expert_forward.
  */
 moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, const float* qscale, int32_t T, void* out,
                          int32_t out_mode, int32_t* err_word, void* stream);

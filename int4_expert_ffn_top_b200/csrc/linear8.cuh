@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, i
 // other.  A lane is a weight row and a column a token, so the 32 lanes of a store write 32 neighbouring outputs of one
 // token.
 // Every wait is bounded: a role whose wait runs out stops and records MOE_ERR_TIMEOUT; copies and MMAs under way are
-// waited for (bounded) before the CTA leaves.
+// waited for (bounded) by the MMAs' thread before the CTAs leave.  (A producer that gives up starves that thread, so it
+// alone sees every copy's end.)
 constexpr int kGM = 128, kGK = 128;
 constexpr int kGEpiWarps = 8, kGThreads = 64 + 32 * kGEpiWarps;
 
@@ -436,10 +437,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           tma_load_pair(sm + s * C::kStage + kGM * kGK, &maps.q, k * kGK, t0, bar);
         }
       }
-      // copies under way: where the stages were used up they have landed (the last ones are waited for by the epilogue)
-#pragma unroll 1
-      for (int q = n > C::kStages ? n - C::kStages : 0; fail && q < n; ++q)
-        tc::bar_wait(empty + q % C::kStages, parity(q, C::kStages), a.timeout_ns);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -469,11 +466,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         }
         if (!fail) commit_pair(acc_full + ab);
       }
-      if (fail) {  // copies and MMAs under way
+      // Nothing of the pair's is under way when it leaves: both CTAs' copies are counted here, at most one for each stage
+      // after the slices used (none where the last slice was), and the MMAs' reads of their operands by `empty`.
 #pragma unroll 1
-        for (int q = n; q < n + C::kStages; ++q) tc::bar_wait(full + q % C::kStages, parity(q, C::kStages), a.timeout_ns / 8);
-        if (n > 0) tc::bar_wait(empty + (n - 1) % C::kStages, parity(n - 1, C::kStages), a.timeout_ns);
-      }
+      for (int q = n; fail && q < n + C::kStages; ++q) tc::bar_wait(full + q % C::kStages, parity(q, C::kStages), a.timeout_ns / 8);
+      if (n > 0) tc::bar_wait(empty + (n - 1) % C::kStages, parity(n - 1, C::kStages), a.timeout_ns);
     }
   } else {
     const int ew = warp - 2, quad = warp & 3, half = ew >> 2, et = tid - 64;
@@ -600,9 +597,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
       tc::tma_load_2d(sm + s * C::kStage, &maps.w, (k0 + n) * kGK, m0, full + s);
       tc::tma_load_2d(sm + s * C::kStage + kGM * kGK, &maps.q, (k0 + n) * kGK, t0, full + s);
     }
-#pragma unroll 1
-    for (int q = n > kSplitStages ? n - kSplitStages : 0; fail && q < n; ++q)  // copies under way
-      tc::bar_wait(full + q % kSplitStages, parity(q), a.timeout_ns);
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = instr_desc_i8(kGM, BN);
 #pragma unroll 1
@@ -611,7 +605,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
       if (!tc::bar_wait(full + s, parity(n), a.timeout_ns)) {
         fail = 1;
         for (int q = n; q < k1 - k0 && q < n + kSplitStages; ++q)  // copies under way
-          tc::bar_wait(full + q % kSplitStages, parity(q), a.timeout_ns);
+          tc::bar_wait(full + q % kSplitStages, parity(q), a.timeout_ns / 8);
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

@@ -290,6 +290,64 @@ def test_call_that_waits_for_room_in_the_queue(cuda_ok):
         assert ((out.double() - ref).abs() <= 3.01 * EPS32 * p.abs() + 1.01 * EPS32 * ref.abs()).all()
 
 
+@pytest.fixture(scope="module")
+def waits(tmp_path_factory):
+    """The product's kernels with a limit of the test's (linear8_waits.cu)."""
+    import ctypes
+    import os
+    import subprocess
+
+    from int4_expert_ffn_top_b200 import _lib, build
+
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    lib = str(tmp_path_factory.mktemp("waits") / "linear8_waits.so")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "linear8_waits.cu")
+    subprocess.run([build.nvcc(), *build.NVCC_FLAGS, "-Xlinker", "-Bsymbolic", "-o", lib, src], check=True)
+    fn = ctypes.CDLL(lib).linear8_waits
+    c = ctypes
+    fn.argtypes = [c.c_int, c.POINTER(_lib.moe_linear8), c.c_void_p, c.c_int64, c.c_void_p, c.c_int32, c.c_void_p, c.c_void_p,
+                   c.c_int64, c.c_int, c.c_void_p]
+    return fn
+
+
+@pytest.mark.parametrize("kind,starve,N,K,T", [(0, 1, 700, 300, 100), (0, 1, 20001, 2048, 200), (0, 1, 256, 4096, 64),
+                                               (1, 1, 700, 300, 30), (1, 2, 700, 2048, 30), (1, 1, 300, 2048, 90)])
+def test_waits_that_run_out(cuda_ok, waits, kind, starve, N, K, T):
+    """Operands that never become complete: the calls end, say so, and leave the multiprocessors as they were (tensor
+    memory, barriers) for the products after them."""
+    import ctypes
+
+    from int4_expert_ffn_top_b200 import _lib
+    lin, W, sw, b = linear(N, K, seed=4)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    ld = M.moe_i8_row_bytes(K)
+    q = torch.randint(-128, 128, (T, ld), dtype=torch.int8, device=DEV, generator=g)
+    sx = torch.rand(T, device=DEV, generator=g) * 0.1
+    out, err = torch.empty((T, N), device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    p, ref = product64(W, sw, b, q, sx, K)
+    tol = 3.01 * EPS32 * p.abs() + 1.01 * EPS32 * ref.abs()
+
+    def call(limit_ns, starved):
+        err.zero_()
+        out.fill_(float("nan"))
+        h = torch.cuda.current_stream().cuda_stream
+        assert waits(kind, ctypes.byref(lin.struct), q.data_ptr(), ld, sx.data_ptr(), T, out.data_ptr(), err.data_ptr(),
+                     limit_ns, starved, h) == _lib.MOE_OK
+        torch.cuda.synchronize()
+        return err.item()
+
+    assert call(2_000_000_000, 0) == 0 and ((out.double() - ref).abs() <= tol).all()
+    for _ in range(3):
+        assert call(20_000_000, starve) == _lib.MOE_ERR_TIMEOUT
+        assert call(2_000_000_000, 0) == 0 and ((out.double() - ref).abs() <= tol).all()
+        M.moe_linear_i8(lin, q, sx, out, M.OUT_F32, err_word=err)
+        torch.cuda.synchronize()
+        assert err.item() == 0 and ((out.double() - ref).abs() <= tol).all()
+    check_linear(4100, 1000, 450, M.OUT_F32)
+    check_linear(4100, 144, 1000, M.OUT_BF16)
+
+
 def test_refusals_on_the_device(cuda_ok):
     """What the quick way does not take is named by the full checks, and nothing is written."""
     lin, *_ = linear(64, 64)

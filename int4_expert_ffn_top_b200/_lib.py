@@ -120,10 +120,13 @@ def binding():
         load()
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"_binding.so not built at {BINDING_PATH}; run int4_expert_ffn_top_b200.build.build()")
-        import torch  # noqa: F401  (the extension needs its libraries)
+        import torch  # the extension needs its libraries
         spec = importlib.util.spec_from_file_location(__package__ + "._binding", BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        if module.built_for != f"moe binding for torch {torch.__version__}":
+            raise RuntimeError(f"{BINDING_PATH} is a {module.built_for}, this is torch {torch.__version__}; run "
+                               "int4_expert_ffn_top_b200.build.build()")
         if not module.load(LIB_PATH):
             raise RuntimeError(f"{BINDING_PATH} does not find its entry points in {LIB_PATH}")
         _fast = module

@@ -1,4 +1,4 @@
-"""Build libmoe.so in-tree with nvcc for sm_100a, and the Python extension beside it with the host compiler."""
+"""Build libmoe.so in-tree with nvcc for sm_100a, and the Python extension beside it with the host compiler and torch's headers."""
 from __future__ import annotations
 
 import os
@@ -33,13 +33,27 @@ def stale(target: str = LIB, deps: list[str] = DEPS) -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def binding_tag() -> str:
+    """What the extension says it was built for (``built_for``)."""
+    import torch
+    return f"moe binding for torch {torch.__version__}"
+
+
+def binding_stale() -> bool:
+    """Its sources are newer, or it was built for another torch."""
+    if stale(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "moe.h")]):
+        return True
+    with open(BINDING, "rb") as f:
+        return binding_tag().encode() + b"\0" not in f.read()
+
+
 def binding_command(out: str) -> list[str]:
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
     inc = [os.path.join(base, "include"), sysconfig.get_path("include"), os.path.join(cuda, "include")]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in inc), "-o", out,
+            f'-DMOE_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in inc), "-o", out,
             BINDING_SOURCE, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
             "-ldl"]
 
@@ -51,7 +65,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(" ".join(cmd), file=sys.stderr)
         subprocess.run(cmd, check=True)
         os.replace(LIB + ".tmp", LIB)
-    if force or stale(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "moe.h")]):
+    if force or binding_stale():
         cmd = binding_command(BINDING + ".tmp")
         if verbose:
             print(" ".join(cmd), file=sys.stderr)

@@ -187,8 +187,18 @@ PyMethodDef methods[] = {
     {"layer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(layer)), METH_FASTCALL, "moe_layer_decode"},
     {nullptr, nullptr, 0, nullptr}};
 
+// The torch that this was built for: its classes are laid out as that one's.
+constexpr char kTorch[] = "moe binding for torch " MOE_TORCH;
+
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", kTorch) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -113,6 +113,16 @@ def test_binding_order_and_checks(rec):  # noqa: F811
     assert len(rec.calls) == n
 
 
+def test_extension_belongs_to_this_torch(lib, monkeypatch):
+    """Built for another torch it is built again, and is not used meanwhile."""
+    assert not B.binding_stale() and _lib.binding().built_for == B.binding_tag()
+    monkeypatch.setattr(torch, "__version__", "2.1.0")
+    assert B.binding_stale()
+    monkeypatch.setattr(_lib, "_fast", None)
+    with pytest.raises(RuntimeError, match="this is torch 2.1.0"):
+        _lib.binding()
+
+
 def test_quick_way_takes_nothing_it_has_not_checked(lib):
     """The extension answers None, without a call, to anything but tensors on the current CUDA device."""
     b = _lib.binding()

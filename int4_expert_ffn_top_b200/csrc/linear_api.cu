@@ -46,9 +46,11 @@ moe_status launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem,
 template <int R, int NT>
 moe_status launch_rows(const l8::LinArgs& a, int nsm, cudaStream_t st) {
   const int groups = (a.N + R - 1) / R;
-  // split K over warps until there are 32 warps a multiprocessor, with a chunk for every lane at least
+  // split K over warps until there are 32 warps a multiprocessor, with a chunk for every lane at least; and as long as a
+  // lane has 16 chunks of a row: fewer rows of many pages are read at once (one and two tokens x 65,536 -> 20,000 191 and
+  // 207 us against 228 and 285, 16,384 -> 16,384 37.9 against 39.5; with 4 chunks 2,048 -> 65,536 21.8 against 20.3)
   int kw = 1;
-  while (kw < l8::kRowWarps && groups * kw < nsm * 32 && a.K16 >= 64 * kw) kw *= 2;
+  while (kw < l8::kRowWarps && (groups * kw < nsm * 32 || a.K16 >= 512 * kw) && a.K16 >= 64 * kw) kw *= 2;
   const int per = l8::kRowWarps / kw;
   return launch_after(l8::rows_kernel<R, NT>, dim3((groups + per - 1) / per), 32 * l8::kRowWarps, 0, 1, st, a, kw);
 }
@@ -217,13 +219,14 @@ moe_status moe_linear_i8(const moe_linear8* W, const int8_t* q, int64_t ldq, con
   const int nsm = multiprocessors(&dev), in = W->in_dim;
   if (nsm < 1) return MOE_ERR_CUDA;
   // Few tokens: dp4a over the weight rows where that is done before a tensor-core kernel has begun (2^24 products take
-  // it 4 us; the cluster split takes 5 for anything small: 3 x 1,008 -> 2,051 2.6 against 5.0 us, but 3 x 2,048 -> 4,096
-  // 8.1 against 5.8 and 8 x 2,048 -> 65,536 65 against 29), and for one or two tokens with rows long enough to keep a
-  // warp's loads going (2,048 -> 65,536: 21.7 against 28.5 us, two tokens 25.6 against 28.6; short rows, 512 -> 200,000:
-  // 39.9 against 30.4, two tokens 1,024 -> 131,072: 35.2 against 29.7).
+  // it 3 to 4 us; the cluster split takes 4.3 for anything small: 3 x 1,008 -> 2,051 2.6 against 5.0 us, 8 x 1,024 ->
+  // 2,048 3.9 against 4.8, but 5 x 2,048 -> 2,048 6.0 against 5.5 and 8 x 2,048 -> 65,536 41 against 29), and for one or
+  // two tokens with rows long enough to keep a warp's loads going (2,048 -> 65,536: 18.6 against 29.2 us, two tokens 21.7
+  // against 29.3; 400 -> 200,000 22.3 against 32.4, two tokens 512 -> 200,000 24.9 against 30.7; short rows, 64 ->
+  // 1,000,000: 104 against 93, two tokens 256 -> 300,000 36.3 against 32.8).
   if (T <= 8) {
     const int nt = T <= 2 ? T : T <= 4 ? 4 : 8;
-    if (static_cast<long long>(a.N) * a.K16 * nt <= 1 << 20 || (T <= 2 && a.K16 >= 64 * T)) {
+    if (static_cast<long long>(a.N) * a.K16 * nt <= 1 << 20 || (T <= 2 && a.K16 >= 24)) {
       if (nt == 1) return launch_rows<4, 1>(a, nsm, st);
       if (nt == 2) return launch_rows<4, 2>(a, nsm, st);
       if (nt == 4) return launch_rows<4, 4>(a, nsm, st);

@@ -152,7 +152,8 @@ def moe_layer_decode(layer: DeviceLayer, u: torch.Tensor | None, K: int, idx: to
 
     Without ``x``, ``u`` (bf16 ``[T, H]``) is the input; with ``x`` (fp32 ``[T, H]``) it receives bf16(rmsnorm(x)),
     or is None.  ``exec_idx`` executes these experts instead of the router's own top-K, which ``idx`` receives.
-    The layer is on the current device, like every tensor.
+    The layer is on the current device, like every tensor.  The quick way in is the current stream's; with ``stream``
+    the call takes about twice the host time (so for moe_quant_i8 and moe_linear_i8).
     """
     fn, L, dev = "moe_layer_decode", layer.struct, getattr(layer, "device", None)
     if stream is None and dev is not None:

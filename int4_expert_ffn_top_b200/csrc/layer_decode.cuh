@@ -35,13 +35,18 @@
 // (1.1 us and more of 22), and behind a norm no hidden vector is that small.
 // Products are exact, group sums and everything after are fp32.
 //
-// What bounds it (B200, 35B shape).  One token, 22 us: the chain of steps; 9.7 MB of weights take 1.5 us, five
-// barriers and hand-overs 1.1 us and more each, the top-K 3, gate/up 3.7, down 3.  16 tokens, 52 us (103 MB, 16 us at
-// copy speed), and 32, 94 us: the instructions around the MMAs.  Eight codes take six to eight half-rate integer operations
-// and two MMAs of which one to three of eight columns are used; the integer pipe is busy 41 % of the time, issue 44 %, shared
-// memory and L1 33 %, DRAM a third.  No single one of them gives way: bringing the weights to L2 ahead of time, the
-// columns to L1 or registers, leaving the unused columns' loads out, or dropping the decoding altogether moves the down
-// loop by less than a tenth each.  16 warps: 8, 12, 20 and 24 take 62, 55, 54 and 55 us for 16 tokens.
+// What bounds it (B200, 35B shape): waiting.  One token, 22 us: the chain of steps; 9.7 MB of weights take 1.5 us.  Up to
+// 4 tokens without routed adapters pass two grid barriers (logits, hidden values), each 1.1 us from arrival to departure
+// and a trip to L2 for the data behind it; images 2.5, router rows 1.6, shared gate/up 0.9, top-K with its barrier 3.2,
+// gate/up 3.6, down with its barrier 4.1, combine 1.8.  16 tokens, 52 us (103 MB, 16 us at copy speed), and 32, 93 us:
+// gate/up 18 and down 15 us of 16 tokens' 52.  Eight codes take six to eight half-rate integer operations and two MMAs of
+// which one to three of eight columns are used, but no pipe is full: issue slots 42 % busy, the integer pipe 38 %, shared
+// memory and L1 29 %, the tensor pipe 11 %, DRAM a third.  Warps wait for instruction fetch, fixed latencies, barriers and
+// loads about alike.  With the columns' loads left out (wrong results) the down loop is a fifth shorter (3.2 of 14.9 us),
+// with the copies left out a tenth (1.3), without the decoding or the shuffles as long; bringing the weights to L2 ahead
+// of time, or the columns to L1 or registers, moves it by less than a tenth each.  What would take the columns' loads
+// away, hidden values read once for several row tiles, is not built.  16 warps: 8, 12, 20 and 24 take 62, 55, 54 and 55 us
+// for 16 tokens.
 #pragma once
 
 #include "common.cuh"

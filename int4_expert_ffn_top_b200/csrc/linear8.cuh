@@ -538,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 // a CTA's slices, or kSplitStages of them, are under way at once), leave their integer sums in shared memory, and each
 // CTA adds up and writes its part of the columns, reading its neighbours' sums through distributed shared memory.
 // Integer sums: the split leaves no trace in the result.  Bound by latency (launch, first bytes of the weights, one join):
-// quantiser and 64 tokens x 2,048 -> 2,048 take 7.9 us, 10 with the tiles of gemm_kernel; 13 x 1,000 -> 2,051 5.1 against
+// quantiser and 64 tokens x 2,048 -> 2,048 take 8.2 us, 10 with the tiles of gemm_kernel; 13 x 1,000 -> 2,051 5.2 against
 // 7.0 us.
 constexpr int kSplitStages = 4, kSplitThreads = 192;
 

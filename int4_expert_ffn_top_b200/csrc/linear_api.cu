@@ -22,7 +22,7 @@ int64_t row_bytes(int32_t n) { return (static_cast<int64_t>(n) + 15) / 16 * 16; 
 bool dim_ok(int32_t n) { return n >= 1 && n <= MOE_I8_MAX_IN; }
 
 // Launch with leave to start while the kernel before it in the stream runs, if that one allows it (the quantiser
-// does): what the kernels here read of its results they read after waiting for it.
+// does): the kernels here set themselves up meanwhile and touch memory after waiting for it.
 template <class... P, class... A>
 moe_status launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, A... args) {
   cudaLaunchAttribute at[2];

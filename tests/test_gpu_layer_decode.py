@@ -464,6 +464,40 @@ def test_two_calls_at_once(cuda_ok):
     assert torch.equal(a.out, ra) and torch.equal(b.out, rb) and a.err.item() == b.err.item() == 0
 
 
+def test_beside_products_on_another_stream(cuda_ok):
+    """The layer on one stream, quantiser and product (rows, cluster split, CTA pairs) on another, many calls in flight:
+    each is as it is alone."""
+    L = Layer(512, 24, 256, 16, down=True)
+    a = Call(L, 11, 4)
+    xa = tokens(11, 512)
+    a(x=xa)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    work = []
+    for N, H, T in ((4096, 2048, 1), (2048, 1024, 40), (8192, 512, 300)):
+        lin = M.DeviceLinear8(torch.randint(-128, 128, (N, H), dtype=torch.int8, device=DEV, generator=g),
+                              torch.rand(N, device=DEV, generator=g))
+        work.append((lin, torch.randn((T, H), device=DEV, generator=g), torch.empty((T, H), dtype=torch.int8, device=DEV),
+                     torch.empty(T, device=DEV), torch.empty((T, N), device=DEV)))
+
+    def products():
+        for lin, x, q, s, out in work:
+            M.moe_quant_i8(x, q, s, eps=EPS)
+            M.moe_linear_i8(lin, q, s, out, M.OUT_F32)
+
+    products()
+    torch.cuda.synchronize()
+    want, outs = a.out.clone(), [w[-1].clone() for w in work]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(60):
+        with torch.cuda.stream(s1):
+            a(x=xa)
+        with torch.cuda.stream(s2):
+            products()
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, want) and a.err.item() == 0
+    assert all(torch.equal(w[-1], o) for w, o in zip(work, outs))
+
+
 def test_agrees_with_route_and_expert_forward(cuda_ok):
     """The library's separate calls on the same layer: the same experts, outputs within their stated tolerance."""
     L = Layer(2048, 64, 512, 16)

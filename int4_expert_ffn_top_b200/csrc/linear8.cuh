@@ -46,6 +46,21 @@ struct QuantArgs {
 // returns nothing, and L2 is where that kernel's writes arrive.)
 MOE_DEV void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 MOE_DEV void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads of what that kernel may have written.  Not through the read-only path (ld.global.nc, __ldg): it is for memory that
+// nothing writes while the kernel runs, and its loads need not stay behind the wait.
+MOE_DEV uint4 load_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+MOE_DEV float load_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
 MOE_DEV void prefetch_to_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Eight neighbouring values of a row, or (VEC false: rows that are not aligned or not whole blocks) one.
@@ -185,7 +200,7 @@ struct LinArgs {
 };
 
 MOE_DEV void store_out(const LinArgs& a, int t, int n, int acc) {
-  const float y = fmaf(static_cast<float>(acc) * a.sx[t], a.sw[n], a.bias ? a.bias[n] : 0.f);
+  const float y = fmaf(static_cast<float>(acc) * load_f32(a.sx + t), load_f32(a.sw + n), a.bias ? load_f32(a.bias + n) : 0.f);
   const size_t o = static_cast<size_t>(t) * a.N + n;
   if (a.out_mode == 1) {
     static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(y);
@@ -233,7 +248,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) rows_kernel(const LinArgs a, i
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = c0 + j * 32 * KW;
-        q[j][i] = c < a.K16 ? ldg_stream(w[i] + 16 * static_cast<size_t>(c)) : make_uint4(0, 0, 0, 0);
+        q[j][i] = c < a.K16 ? load_stream(w[i] + 16 * static_cast<size_t>(c)) : make_uint4(0, 0, 0, 0);
       }
     // one token: all of these loads before the codes' (mixed, 20.9 us for 2,048 -> 65,536 in place of 19.2); with more the
     // codes' are as many, and best among them (two tokens, 2,048 -> 4,096: 5.0 us against 6.2)
@@ -482,10 +497,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const int ab = it & 1, m0 = (t % a.m_tiles) * 2 * kGM + rank * kGM, t0 = (t / a.m_tiles) * BN;
       const int n = m0 + quad * 32 + lane;
       const bool row = n < a.lin.N;
-      const float sw = row ? __ldg(a.lin.sw + n) : 0.f, bias = row && a.lin.bias ? __ldg(a.lin.bias + n) : 0.f;
+      const float sw = row ? load_f32(a.lin.sw + n) : 0.f, bias = row && a.lin.bias ? load_f32(a.lin.bias + n) : 0.f;
       float* sx = sxs + ab * BN;
 #pragma unroll 1
-      for (int i = et; i < BN; i += 32 * kGEpiWarps) sx[i] = t0 + i < a.lin.T ? __ldg(a.lin.sx + t0 + i) : 0.f;
+      for (int i = et; i < BN; i += 32 * kGEpiWarps) sx[i] = t0 + i < a.lin.T ? load_f32(a.lin.sx + t0 + i) : 0.f;
       // the eight warps go on together or not at all (and see the scales)
       if (epi_any(!tc::bar_wait(acc_full + ab, parity(it, 2), a.timeout_ns))) {
         fail = 1;
@@ -617,6 +632,14 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     tc::mma_commit(done);  // (of what was issued, where a wait ran out)
   }
   __syncwarp();
+  dependency_wait();
+  float sw[2], bias[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = min(m0 + (tid & 63) + 64 * h, a.lin.N - 1);
+    sw[h] = load_f32(a.lin.sw + n);
+    bias[h] = a.lin.bias ? load_f32(a.lin.bias + n) : 0.f;
+  }
   if (!tc::bar_wait(done, 0, 2 * a.timeout_ns)) fail = 1;
   if (fail) report(a.err, 5 /* MOE_ERR_TIMEOUT */);
   __syncwarp();
@@ -634,12 +657,12 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
-  dependency_wait();
   cluster_sync();
   {
     // a thread per (row, column): rank takes every S-th column; 192 threads: row = tid % 64 (+ 64), column = tid / 64
 #pragma unroll 1
     for (int c = rank + S * (tid >> 6); c < BN && t0 + c < a.lin.T; c += 3 * S) {
+      const float sx = load_f32(a.lin.sx + t0 + c);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = (tid & 63) + 64 * h, n = m0 + row;
@@ -655,8 +678,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split_kernel(const __grid_co
         }
 #pragma unroll
         for (int p = 0; p < 8; ++p) v += x[p];
-        const float y = fmaf(static_cast<float>(v) * __ldg(a.lin.sx + t0 + c), __ldg(a.lin.sw + n),
-                             a.lin.bias ? __ldg(a.lin.bias + n) : 0.f);
+        const float y = fmaf(static_cast<float>(v) * sx, sw[h], bias[h]);
         const size_t o = static_cast<size_t>(t0 + c) * a.lin.N + n;
         if (MODE == 1) {
           static_cast<__nv_bfloat16*>(a.lin.out)[o] = __float2bfloat16_rn(y);

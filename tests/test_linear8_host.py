@@ -75,6 +75,17 @@ def test_library_refuses_addresses_that_no_element_can_have(lib):
         assert lib.moe_linear_i8(ctypes.byref(W), A, 64, qs, 1, out, mode, err, None) == bad
 
 
+def test_product_takes_no_read_only_loads():
+    """What the kernel ahead may be writing when the product starts is not read through the read-only path, whose loads a
+    compiler may move above the wait for that kernel."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(B.__file__), "csrc", "linear8.cuh")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert "griddepcontrol.wait" in code
+    assert not re.findall(r"__ldg|ldg_stream|global\.nc|__restrict__", code)
+
+
 class FakeLinear:
     def __init__(self, n, k):
         self.struct = _lib.moe_linear8(1 << 20, (k + 15) // 16 * 16, 1 << 20, None, n, k)

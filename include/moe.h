@@ -232,10 +232,11 @@ size_t moe_workspace_size(const moe_layer* L, int32_t T, int32_t K);
  *   exactly, and so do the entries of u (in any range: no MOE_ERR_RANGE for it)
  *   down to 2^-22 of their token's largest; smaller ones are rounded by at most
  *   2^-30 of it.  Hidden values are stored unscaled: 22 significant bits down to
- *   |h| = 2^-14, rounded by at most 2^-36 below it.  So where u is given and small
- *   (a norm never makes it so) an output is off by up to 2^-36 sqrt(I) times the
- *   largest singular value of each down projection; with u about 1e-3 that is a
- *   1e-5th of it, with u about 1e-4 a 1e-3rd, and outputs of u below 1e-6 are lost.
+ *   |h| = 2^-14, rounded by at most 2^-36 below it.  So where u is small (given so,
+ *   or normed with mean(x^2) far below eps) an output is off by up to 2^-36 sqrt(I)
+ *   times the largest singular value of each down projection; with u about 1e-3
+ *   that is a 1e-5th of it, with u about 1e-4 a 1e-3rd, and outputs of u below 1e-6
+ *   are lost.
  *   A finite hidden value beyond fp16's range (|h| > 65504) stores MOE_ERR_RANGE in
  *   err_word and leaves that token's output undefined.
  * workspace: at least moe_layer_decode_workspace_size(L, T, K) bytes, 256-byte

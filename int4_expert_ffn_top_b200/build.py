@@ -1,4 +1,5 @@
-"""Build libmoe.so in-tree with nvcc for sm_100a, and the Python extension beside it with the host compiler and torch's headers."""
+"""Build libmoe.so in-tree with nvcc for sm_100a, and the Python extension beside it with the host compiler and torch's
+headers."""
 from __future__ import annotations
 
 import os
@@ -53,8 +54,8 @@ def binding_command(out: str) -> list[str]:
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
     inc = [os.path.join(base, "include"), sysconfig.get_path("include"), os.path.join(cuda, "include")]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-            f'-DMOE_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in inc), "-o", out,
-            BINDING_SOURCE, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            f'-DMOE_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{d}" for d in inc), "-o", out, BINDING_SOURCE, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
             "-ldl"]
 
 

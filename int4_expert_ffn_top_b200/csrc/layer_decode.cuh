@@ -32,7 +32,8 @@
 // and 2^11 (h - hi), 22 bits together, in two columns of the N side.  They are stored
 // unscaled: below 2^-14 what stays is an absolute 2^-36.  A power of two for each row
 // would need the row's largest value, which only another exchange between all CTAs gives
-// (1.1 us and more of 22), and behind a norm no hidden vector is that small.
+// (1.1 us and more of 22), and normed tokens have no hidden vectors that small (unless
+// mean(x^2) is far below eps).
 // Products are exact, group sums and everything after are fp32.
 //
 // What bounds it (B200, 35B shape): waiting.  One token, 22 us: the chain of steps; 9.7 MB of weights take 1.5 us.  Up to

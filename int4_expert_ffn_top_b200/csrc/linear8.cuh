@@ -481,8 +481,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         }
         if (!fail) commit_pair(acc_full + ab);
       }
-      // Nothing of the pair's is under way when it leaves: both CTAs' copies are counted here, at most one for each stage
-      // after the slices used (none where the last slice was), and the MMAs' reads of their operands by `empty`.
+      // Nothing of the pair's is under way when it leaves: both CTAs' copies are counted here (after a failure at most one
+      // for each stage beyond the slices used), and `empty` says that the MMAs are done with their operands.
 #pragma unroll 1
       for (int q = n; fail && q < n + C::kStages; ++q) tc::bar_wait(full + q % C::kStages, parity(q, C::kStages), a.timeout_ns / 8);
       if (n > 0) tc::bar_wait(empty + (n - 1) % C::kStages, parity(n - 1, C::kStages), a.timeout_ns);

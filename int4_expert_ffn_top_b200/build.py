@@ -55,8 +55,8 @@ def binding_command(out: str) -> list[str]:
     inc = [os.path.join(base, "include"), sysconfig.get_path("include"), os.path.join(cuda, "include")]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             f'-DMOE_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            *(f"-I{d}" for d in inc), "-o", out, BINDING_SOURCE, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
-            "-ldl"]
+            *(f"-I{d}" for d in inc), "-o", out, BINDING_SOURCE, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python", "-ldl"]
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
